@@ -66,6 +66,8 @@ extern "C" {
 #define LLAMA_ERR_TOKEN_RANGE -10 /* device flag: a token id outside [0, vocab_size) */
 #define LLAMA_ERR_POS_RANGE -11   /* device flag: start_pos[b] + s outside [0, max_seq_len) */
 #define LLAMA_ERR_TIMEOUT -12     /* device flag: a bounded in-kernel wait gave up */
+#define LLAMA_ERR_PAGE_RANGE -13  /* device flag: a block-table entry, free page or slot outside the pool */
+#define LLAMA_ERR_OUT_OF_PAGES -14 /* device flag: a page plan needs more pages than are free */
 
 /* GEMM path selection for llama_linear (diagnostics) */
 #define LLAMA_PATH_AUTO 0
@@ -450,6 +452,150 @@ int llama_linear_noalloc(const void* x_dev, const void* w_dev, float* y_dev, int
  * *flags (if not NULL) receives the raw bits (4 = timeout). Allocates nothing.
  */
 int llama_linear_noalloc_status(int* flags);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Serving operators over a paged KV-cache
+ *
+ * The pages have no counterpart (their cache is one contiguous block per batch
+ * slot); the attention computed is the notes' Attention.forward with the cached
+ * causal mask of "灵哥讲llama3(中)", request by request. A pool of K pages and
+ * one of V pages, each [num_pages][n_kv_heads][page_size][head_dim] in the
+ * storage type, hold the tokens of every request; row b of block_tables
+ * (int32 [n_seqs][max_pages]) lists the pages of request b in the order of its
+ * positions; token p of request b sits in row p % page_size of page
+ * block_tables[b][p / page_size], and its slot number is
+ * page * page_size + p % page_size. The new tokens of all requests are packed
+ * without padding: request b holds rows cu[b] .. cu[b + 1] - 1 of every
+ * [n_tokens] array (cu int32 [n_seqs + 1], cu[0] = 0).
+ *
+ * Common to these calls (llama_page_plan to llama_attn_packed):
+ *  - they run on the current device, on cuda_stream, asynchronously; they
+ *    allocate nothing and keep nothing between calls, so they can be captured;
+ *    pointers are device pointers on that device.
+ *  - lengths, tables and slots are read on the device. What only the device
+ *    can see is OR-ed into *status_dev (int32, zeroed by the caller once): bits
+ *    2 (position range), 4 (timeout), 8 (page range), 16 (out of pages);
+ *    llama_paged_status reads it back. Nothing outside the given arrays is
+ *    read or written, whatever the lengths, tables and slots hold.
+ *  - row strides are in elements, at least the row's width, and multiples of
+ *    16 bytes; tensors start on 16-byte boundaries; inputs and outputs do not
+ *    overlap except where a call says so. n_seqs <= LLAMA_MAX_SEQS.
+ */
+#define LLAMA_MAX_SEQS 4096
+
+/*
+ * Shape of a paged cache. Rules: dtype LLAMA_FP32 or LLAMA_BF16; n_heads a
+ * multiple of n_kv_heads; head_dim 64 or 128; page_size 16, 32, 64 or 128
+ * tokens; num_pages >= 1 with num_pages * n_kv_heads * page_size < 2^31;
+ * max_pages >= 1 (columns of block_tables) with max_pages * page_size < 2^31.
+ */
+typedef struct {
+  int32_t dtype;
+  int32_t n_heads;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t num_pages;
+  int32_t max_pages;
+} llama_page_args;
+
+/*
+ * Plan a step: block tables, slots and packing from the requests' lengths.
+ * Request b holds cached_lens_dev[b] tokens in the pages of its row of
+ * block_tables_dev and gets new_lens_dev[b] more. For each request, in order,
+ * the pages it lacks are taken from the top of the free stack
+ * (free_pages_dev[0 .. free_count - 1], free_count = *free_count_dev: entry
+ * free_count - 1 first) and written to its row. new_lens_dev[b] < 0 ends
+ * request b: its ceil(cached / page_size) pages go back on the stack, in
+ * (request, column) order, after every page of this call has been taken.
+ * Written: block_tables_dev (new entries only), free_pages_dev (returned pages
+ * only), *free_count_out_dev, cu_dev [n_seqs + 1], kv_lens_dev [n_seqs]
+ * (cached + new; 0 for an ended request), positions_dev and slots_dev
+ * [max_tokens] (position and slot of each packed token; 0 and -1 behind the
+ * last one). free_count_out_dev may be free_count_dev, and kv_lens_dev may be
+ * cached_lens_dev. A plan that cannot be met changes nothing but the outputs:
+ * cu all 0, kv_lens = cached, slots all -1, the free count as it was, and the
+ * flag says why (out of pages: more needed than free, or a count outside
+ * [0, num_pages]; position range: a negative length, a request past
+ * max_pages * page_size tokens, or more new tokens than max_tokens). A page
+ * number outside the pool raises the page range flag; its tokens get slot -1,
+ * and where an ended request lists one, -1 goes on the stack in its place.
+ * Uses page_size, num_pages and max_pages of args.
+ */
+int llama_page_plan(const llama_page_args* args, const int32_t* cached_lens_dev, const int32_t* new_lens_dev,
+                    int n_seqs, int max_tokens, int32_t* block_tables_dev, int32_t* free_pages_dev,
+                    const int32_t* free_count_dev, int32_t* free_count_out_dev, int32_t* cu_dev,
+                    int32_t* kv_lens_dev, int32_t* positions_dev, int32_t* slots_dev, int32_t* status_dev,
+                    void* cuda_stream);
+
+/*
+ * RoPE and the cache append for packed tokens. Row t of qkv_dev (qkv_stride
+ * elements apart, type qkv_dtype: LLAMA_FP32, or LLAMA_BF16 with bf16 pages)
+ * holds q [n_heads][head_dim], k [n_kv_heads][head_dim], v alike. The pairs
+ * (2i, 2i + 1) of q and k turn by the angle of row positions_dev[t] of
+ * rope_dev (fp32 [n_pos][head_dim / 2][2]: cos, sin; the notes'
+ * apply_rotary_emb), in fp32, rounded once to the storage type; q goes to
+ * q_out_dev [n_tokens][n_heads][head_dim], k and v to slot slots_dev[t] of the
+ * pools. A token with slot -1 is skipped (its q_out row stays as it was); a
+ * position outside [0, n_pos) or a slot outside the pool skips it and raises
+ * the position or page range flag. Slots other than -1 are distinct.
+ */
+int llama_rope_append(const llama_page_args* args, const void* qkv_dev, int64_t qkv_stride, int qkv_dtype,
+                      const int32_t* positions_dev, const int32_t* slots_dev, int n_tokens, const float* rope_dev,
+                      int n_pos, void* q_out_dev, void* k_pages_dev, void* v_pages_dev, int32_t* status_dev,
+                      void* cuda_stream);
+
+/*
+ * Bytes of workspace that llama_attn_paged and llama_attn_packed need for
+ * these shapes (whatever the lengths), or LLAMA_ERR_INVALID_ARGS. The caller
+ * zeroes the workspace once; every call leaves its counters zeroed again. A
+ * workspace serves one call at a time: calls (or graphs) that may overlap take
+ * one each. After a timeout flag it is zeroed again before its next use.
+ */
+int64_t llama_attn_workspace_bytes(int dtype, int n_heads, int n_kv_heads, int head_dim);
+
+/*
+ * Attention of new tokens over a paged cache. Request b has n = cu[b + 1] -
+ * cu[b] new tokens (rows cu[b] .. of q_dev, q_stride elements apart, each
+ * [n_heads][head_dim]) and kv_lens_dev[b] cached tokens, the new ones already
+ * among them. Its i-th new token stands at position p = kv_len - n + i; head h
+ * of it sees keys 0 .. p of kv head h / (n_heads / n_kv_heads):
+ * out = softmax(q.k / sqrt(head_dim)) V, fp32 scores and sums, to the same row
+ * of out_dev [n_tokens][n_heads][head_dim]. A row that sees no key (p < 0) is
+ * zero. What the pages hold past a request's kv_len, and pages that no table
+ * lists, do not matter, whatever they hold. max_new: the most new tokens of
+ * one request (1: the single-token kernel). Requests with no new tokens, and
+ * rows of no request, are left as they were. A request whose cu or kv_len
+ * break the rules (cu not ascending within [0, n_tokens], more than max_new
+ * tokens, kv_len outside [0, max_pages * page_size]) is skipped and raises the
+ * position range flag; a table entry outside the pool raises the page range
+ * flag and counts as keys and values of zero. The order of sums depends on the
+ * lengths only: equal calls give equal bits.
+ */
+int llama_attn_paged(const llama_page_args* args, const void* q_dev, int64_t q_stride, const void* k_pages_dev,
+                     const void* v_pages_dev, const int32_t* block_tables_dev, const int32_t* cu_dev,
+                     const int32_t* kv_lens_dev, int n_seqs, int n_tokens, int max_new, void* out_dev,
+                     void* workspace_dev, int64_t workspace_bytes, int32_t* status_dev, void* cuda_stream);
+
+/*
+ * Causal attention over packed prompts: sequence b holds rows cu[b] ..
+ * cu[b + 1] - 1 of q, k and v (strides in elements; rows [n_heads][head_dim]
+ * and [n_kv_heads][head_dim]: a fused QKV matrix serves as all three), its
+ * i-th token sees its tokens 0 .. i. Otherwise as llama_attn_paged with
+ * max_len for max_new.
+ */
+int llama_attn_packed(int dtype, int n_heads, int n_kv_heads, int head_dim, const void* q_dev, int64_t q_stride,
+                      const void* k_dev, int64_t k_stride, const void* v_dev, int64_t v_stride,
+                      const int32_t* cu_dev, int n_seqs, int n_tokens, int max_len, void* out_dev,
+                      void* workspace_dev, int64_t workspace_bytes, int32_t* status_dev, void* cuda_stream);
+
+/*
+ * Synchronise the device, return and clear *status_dev: LLAMA_OK or the most
+ * severe of LLAMA_ERR_TIMEOUT, LLAMA_ERR_PAGE_RANGE, LLAMA_ERR_OUT_OF_PAGES,
+ * LLAMA_ERR_POS_RANGE; *flags (if not NULL) receives the raw bits.
+ */
+int llama_paged_status(int32_t* status_dev, int* flags);
 
 #ifdef __cplusplus
 }

@@ -28,6 +28,9 @@ LLAMA_ERR_INTERNAL = -6
 LLAMA_ERR_TOKEN_RANGE = -10
 LLAMA_ERR_POS_RANGE = -11
 LLAMA_ERR_TIMEOUT = -12
+LLAMA_ERR_PAGE_RANGE = -13
+LLAMA_ERR_OUT_OF_PAGES = -14
+LLAMA_MAX_SEQS = 4096
 LLAMA_PATH_AUTO, LLAMA_PATH_TCGEN05, LLAMA_PATH_GEMV, LLAMA_PATH_SIMT = 0, 1, 2, 3
 LLAMA_WEIGHTS_TILED = 16
 LLAMA_DECODE_AUTO, LLAMA_DECODE_LAYERED, LLAMA_DECODE_PERSISTENT = 0, 1, 2
@@ -41,7 +44,8 @@ EXPORTED = ("llama_ffn_hidden", "llama_create", "llama_destroy", "llama_set_laye
             "llama_linear_noalloc", "llama_linear_noalloc_status", "llama_sample", "llama_generate", "llama_set_decode_kernel",
             "llama_set_decode_attention", "llama_set_decode_linear_mma", "llama_tile_weights",
             "llama_selftest_bounded_wait", "llama_set_alloc_limit", "llama_allocated_bytes",
-            "llama_selfcheck_plans")
+            "llama_selfcheck_plans", "llama_page_plan", "llama_rope_append", "llama_attn_workspace_bytes",
+            "llama_attn_paged", "llama_attn_packed", "llama_paged_status")
 
 
 class LlamaArgs(ctypes.Structure):
@@ -50,6 +54,12 @@ class LlamaArgs(ctypes.Structure):
                 ("ffn_dim_multiplier", ctypes.c_float), ("norm_eps", ctypes.c_float), ("rope_theta", ctypes.c_float),
                 ("max_batch_size", ctypes.c_int32), ("max_seq_len", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("rope_half_split", ctypes.c_int32)]
+
+
+class LlamaPageArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
 
 
 class LlamaError(RuntimeError):
@@ -99,10 +109,18 @@ def lib() -> ctypes.CDLL:
         L.llama_set_alloc_limit.argtypes = [ctypes.c_uint64]
         L.llama_allocated_bytes.argtypes = []
         L.llama_selfcheck_plans.argtypes = [i] * 7
+        pa, i64 = ctypes.POINTER(LlamaPageArgs), ctypes.c_int64
+        L.llama_page_plan.argtypes = [pa, vp, vp, i, i] + [vp] * 10
+        L.llama_rope_append.argtypes = [pa, vp, i64, i, vp, vp, i, vp, i, vp, vp, vp, vp, vp]
+        L.llama_attn_workspace_bytes.argtypes = [i] * 4
+        L.llama_attn_paged.argtypes = [pa, vp, i64] + [vp] * 5 + [i, i, i, vp, vp, i64, vp, vp]
+        L.llama_attn_packed.argtypes = [i] * 4 + [vp, i64] * 3 + [vp, i, i, i, vp, vp, i64, vp, vp]
+        L.llama_paged_status.argtypes = [vp, ctypes.POINTER(i)]
         for name in EXPORTED:
             if name not in ("llama_destroy", "llama_strerror"):
                 getattr(L, name).restype = ctypes.c_int
         L.llama_allocated_bytes.restype = ctypes.c_uint64
+        L.llama_attn_workspace_bytes.restype = ctypes.c_int64
         _lib = L
     return _lib
 
@@ -310,6 +328,149 @@ def llama_linear_noalloc_status():
     """(code, raw error bits) of llama_linear_noalloc on the current device; clears them."""
     flags = ctypes.c_int(0)
     code = lib().llama_linear_noalloc_status(ctypes.byref(flags))
+    return code, flags.value
+
+
+# ---- serving operators over a paged cache. Their calls run on the current
+# device, so tensors of another device (or of the CPU) are refused here.
+_TORCH = {"fp32": torch.float32, "bf16": torch.bfloat16}
+_CODE = {torch.float32: LLAMA_FP32, torch.bfloat16: LLAMA_BF16}
+
+
+@dataclass
+class PageArgs:
+    """llama_page_args: heads and storage type of a paged cache, its page size, pages and table width."""
+    n_heads: int
+    n_kv_heads: int
+    head_dim: int
+    page_size: int
+    num_pages: int
+    max_pages: int
+    dtype: str = "bf16"
+
+    def __post_init__(self):
+        if self.dtype not in _TORCH:
+            raise ValueError(f"dtype {self.dtype!r}: 'fp32' or 'bf16'")
+
+    def c(self) -> LlamaPageArgs:
+        return LlamaPageArgs(LLAMA_BF16 if self.dtype == "bf16" else LLAMA_FP32, self.n_heads, self.n_kv_heads,
+                             self.head_dim, self.page_size, self.num_pages, self.max_pages)
+
+
+def _on_device(name: str, t: torch.Tensor, dtype, device: int) -> int:
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError(f"{name} must be on the current device cuda:{device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _whole(name: str, t: torch.Tensor, dtype, shape, device: int) -> int:
+    """Pointer of a contiguous tensor of this type and shape (-1: any extent)."""
+    p = _on_device(name, t, dtype, device)
+    if len(t.shape) != len(shape) or any(w != -1 and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return p
+
+
+def _rows(name: str, t: torch.Tensor, dtype, n: int, heads: int, head_dim: int, device: int):
+    """Pointer and row stride of [n][heads][head_dim] rows that may stand apart (a slice of a wider matrix)."""
+    p = _on_device(name, t, dtype, device)
+    if tuple(t.shape) != (n, heads, head_dim):
+        raise ValueError(f"{name} must have shape {(n, heads, head_dim)}, got {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != head_dim):
+        raise ValueError(f"{name}: the values of a row must be contiguous")
+    return p, (s0 if n > 1 else heads * head_dim)
+
+
+def llama_page_plan(args: PageArgs, cached_lens: torch.Tensor, new_lens: torch.Tensor, block_tables: torch.Tensor,
+                    free_pages: torch.Tensor, free_count: torch.Tensor, free_count_out: torch.Tensor,
+                    cu: torch.Tensor, kv_lens: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+                    status: torch.Tensor, stream=None) -> None:
+    """All int32: lengths [n_seqs], block_tables [n_seqs][max_pages], free_pages [num_pages], counts and status [1],
+    cu [n_seqs + 1], positions and slots [max_tokens]."""
+    d, i32 = torch.cuda.current_device(), torch.int32
+    n, T = cached_lens.shape[0], positions.shape[0]
+    _check(lib().llama_page_plan(
+        ctypes.byref(args.c()), _whole("cached_lens", cached_lens, i32, (n,), d), _whole("new_lens", new_lens, i32, (n,), d),
+        n, T, _whole("block_tables", block_tables, i32, (n, args.max_pages), d),
+        _whole("free_pages", free_pages, i32, (args.num_pages,), d), _whole("free_count", free_count, i32, (1,), d),
+        _whole("free_count_out", free_count_out, i32, (1,), d), _whole("cu", cu, i32, (n + 1,), d),
+        _whole("kv_lens", kv_lens, i32, (n,), d), _whole("positions", positions, i32, (T,), d),
+        _whole("slots", slots, i32, (T,), d), _whole("status", status, i32, (1,), d), _stream(stream)), "llama_page_plan")
+
+
+def llama_rope_append(args: PageArgs, qkv: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+                      rope: torch.Tensor, q_out: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                      status: torch.Tensor, stream=None) -> None:
+    """qkv [n][(n_heads + 2 n_kv_heads) head_dim] fp32 or the storage type (rows may stand apart); rope fp32
+    [n_pos][head_dim / 2][2]; q_out [n][n_heads][head_dim]; pools [num_pages][n_kv_heads][page_size][head_dim]."""
+    d, i32, dt = torch.cuda.current_device(), torch.int32, _TORCH[args.dtype]
+    n, D = qkv.shape[0], args.head_dim
+    width = (args.n_heads + 2 * args.n_kv_heads) * D
+    if qkv.dtype not in (torch.float32, dt):
+        raise ValueError(f"qkv must be torch.float32 or {dt}, got {qkv.dtype}")
+    if qkv.dim() != 2 or qkv.shape[1] != width or qkv.stride(1) != 1:
+        raise ValueError(f"qkv must have shape (n, {width}) with contiguous rows, got {tuple(qkv.shape)}")
+    pool = (args.num_pages, args.n_kv_heads, args.page_size, D)
+    _check(lib().llama_rope_append(
+        ctypes.byref(args.c()), _on_device("qkv", qkv, qkv.dtype, d), qkv.stride(0) if n > 1 else width, _CODE[qkv.dtype],
+        _whole("positions", positions, i32, (n,), d), _whole("slots", slots, i32, (n,), d), n,
+        _whole("rope", rope, torch.float32, (-1, D // 2, 2), d), rope.shape[0],
+        _whole("q_out", q_out, dt, (n, args.n_heads, D), d), _whole("k_pages", k_pages, dt, pool, d),
+        _whole("v_pages", v_pages, dt, pool, d), _whole("status", status, i32, (1,), d), _stream(stream)),
+        "llama_rope_append")
+
+
+def llama_attn_workspace_bytes(n_heads: int, n_kv_heads: int, head_dim: int, dtype: str = "bf16") -> int:
+    """Bytes of the (zeroed, uint8) workspace of llama_attn_paged and llama_attn_packed."""
+    n = lib().llama_attn_workspace_bytes(LLAMA_BF16 if dtype == "bf16" else LLAMA_FP32, n_heads, n_kv_heads, head_dim)
+    if n < 0:
+        raise LlamaError(n, "llama_attn_workspace_bytes")
+    return n
+
+
+def llama_attn_paged(args: PageArgs, q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                     block_tables: torch.Tensor, cu: torch.Tensor, kv_lens: torch.Tensor, max_new: int,
+                     out: torch.Tensor, workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+    """q [n][n_heads][head_dim] (rows may stand apart), out contiguous of the same shape; cu [n_seqs + 1]."""
+    d, i32, dt = torch.cuda.current_device(), torch.int32, _TORCH[args.dtype]
+    n, B, D = q.shape[0], kv_lens.shape[0], args.head_dim
+    pool = (args.num_pages, args.n_kv_heads, args.page_size, D)
+    qp, qs = _rows("q", q, dt, n, args.n_heads, D, d)
+    _check(lib().llama_attn_paged(
+        ctypes.byref(args.c()), qp, qs, _whole("k_pages", k_pages, dt, pool, d), _whole("v_pages", v_pages, dt, pool, d),
+        _whole("block_tables", block_tables, i32, (B, args.max_pages), d), _whole("cu", cu, i32, (B + 1,), d),
+        _whole("kv_lens", kv_lens, i32, (B,), d), B, n, int(max_new), _whole("out", out, dt, (n, args.n_heads, D), d),
+        _whole("workspace", workspace, torch.uint8, (-1,), d), workspace.shape[0],
+        _whole("status", status, i32, (1,), d), _stream(stream)), "llama_attn_paged")
+
+
+def llama_attn_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, max_len: int,
+                      out: torch.Tensor, workspace: torch.Tensor, status: torch.Tensor, stream=None) -> None:
+    """q [n][n_heads][head_dim], k and v [n][n_kv_heads][head_dim] (rows may stand apart); out contiguous like q."""
+    d, i32, dt = torch.cuda.current_device(), torch.int32, q.dtype
+    if dt not in _CODE:
+        raise ValueError(f"q must be torch.float32 or torch.bfloat16, got {dt}")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be [tokens][heads][head_dim]")
+    (n, H, D), Hkv = q.shape, k.shape[1]
+    qp, qs = _rows("q", q, dt, n, H, D, d)
+    kp, ks = _rows("k", k, dt, n, Hkv, D, d)
+    vp, vs = _rows("v", v, dt, n, Hkv, D, d)
+    _check(lib().llama_attn_packed(
+        _CODE[dt], H, Hkv, D, qp, qs, kp, ks, vp, vs, _whole("cu", cu, i32, (-1,), d), cu.shape[0] - 1, n, int(max_len),
+        _whole("out", out, dt, (n, H, D), d), _whole("workspace", workspace, torch.uint8, (-1,), d), workspace.shape[0],
+        _whole("status", status, i32, (1,), d), _stream(stream)), "llama_attn_packed")
+
+
+def llama_paged_status(status: torch.Tensor):
+    """(code, raw bits) of a status word, after synchronising; clears it."""
+    flags = ctypes.c_int(0)
+    code = lib().llama_paged_status(_ptr(status), ctypes.byref(flags))
     return code, flags.value
 
 

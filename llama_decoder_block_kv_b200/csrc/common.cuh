@@ -16,6 +16,8 @@
 #define LLAMA_DEV_TOKEN_RANGE 1
 #define LLAMA_DEV_POS_RANGE 2
 #define LLAMA_DEV_TIMEOUT 4
+#define LLAMA_DEV_PAGE_RANGE 8
+#define LLAMA_DEV_OUT_OF_PAGES 16
 
 // about one second of waiting before an mbarrier wait gives up
 #ifndef LLAMA_WAIT_LIMIT_NS

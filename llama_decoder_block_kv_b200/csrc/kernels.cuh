@@ -166,6 +166,84 @@ cudaError_t launch_attn_simple(const void* q, const void* ck, const void* cv, vo
                                int B, int T_, int H, int Hkv, int D, int S_max, cudaStream_t st);
 
 
+// ---- serving operators over a paged cache (paged_api.cu checks the arguments)
+
+// page_plan.cu
+struct PagePlanParams {
+  const int* cached;
+  const int* fresh;  // new tokens of each request; < 0 ends it
+  int B, max_tokens, page_shift, num_pages, max_pages;
+  int* tables;       // [B][max_pages]
+  int* free_pages;
+  const int* free_count;
+  int* free_count_out;
+  int* cu;
+  int* kv_lens;
+  int* positions;
+  int* slots;
+  int* status;
+};
+cudaError_t launch_page_plan(const PagePlanParams& p, cudaStream_t st);
+
+// rope_append.cu
+struct RopeAppendParams {
+  const void* qkv;
+  long long stride;
+  const int* positions;
+  const int* slots;
+  int N, H, Hkv, D, page_shift, num_pages, n_pos;
+  const float2* rope;
+  void* q_out;
+  void* k_pages;
+  void* v_pages;
+  int* status;
+};
+// in_bf16 / out_bf16: types of qkv and of q_out and the pools
+cudaError_t launch_rope_append(const RopeAppendParams& p, bool in_bf16, bool out_bf16, cudaStream_t st);
+
+// Attention of packed rows, over pages (tables != nullptr) or over packed K, V rows.
+struct RaggedAttnParams {
+  const void* q;
+  long long q_stride;
+  const void* k;  // pools [num_pages][Hkv][ps][D], or rows [N][Hkv][D] k_stride apart
+  const void* v;
+  long long k_stride, v_stride;  // packed rows only
+  const int* tables;   // [B][max_pages], or nullptr
+  const int* cu;       // [B + 1]
+  const int* kv_lens;  // [B] (paged)
+  int B, N, max_new;
+  int H, Hkv, D;
+  int page_shift, num_pages, max_pages;
+  void* o;
+  int* status;
+};
+
+// Request b's new tokens and keys, from device memory, with the checks of the
+// header: false (and the position range flag) for a request that is skipped.
+struct RaggedSeq {
+  int q0, n_new, kv;  // first row, new tokens, keys
+};
+__device__ __forceinline__ bool ragged_seq(const RaggedAttnParams& p, int b, RaggedSeq& s, bool flag) {
+  const int c0 = p.cu[b], c1 = p.cu[b + 1];
+  s.q0 = c0;
+  s.n_new = c1 - c0;
+  bool ok = c0 >= 0 && c1 >= c0 && c1 <= p.N && s.n_new <= p.max_new;
+  s.kv = ok ? s.n_new : 0;
+  if (p.tables && ok) {
+    s.kv = p.kv_lens[b];
+    ok = s.kv >= 0 && s.kv <= (p.max_pages << p.page_shift);
+  }
+  if (!ok) {
+    s.n_new = s.kv = 0;
+    if (flag) atomicOr(p.status, LLAMA_DEV_POS_RANGE);
+  }
+  return ok;
+}
+
+// attn_ragged.cu
+template <typename T>
+cudaError_t launch_attn_ragged_rows(const RaggedAttnParams& p, cudaStream_t st);
+
 // decode_block.cu: one decode step of a whole block in one persistent launch
 constexpr int DB_RING_STAGES = 9;                 // 16 KB weight tiles in flight per SM
 constexpr uint32_t DB_AREA_BYTES = 64 * 1024;     // x slice of a linear / K,V tiles of the attention

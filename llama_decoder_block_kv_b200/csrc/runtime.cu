@@ -905,6 +905,8 @@ const char* llama_strerror(int code) {
     case LLAMA_ERR_TOKEN_RANGE: return "token id outside [0, vocab_size)";
     case LLAMA_ERR_POS_RANGE: return "position outside [0, max_seq_len)";
     case LLAMA_ERR_TIMEOUT: return "a bounded device wait timed out";
+    case LLAMA_ERR_PAGE_RANGE: return "page or slot outside the pool";
+    case LLAMA_ERR_OUT_OF_PAGES: return "not enough free pages";
     default: return "unknown error";
   }
 }
