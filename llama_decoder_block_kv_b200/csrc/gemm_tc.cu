@@ -504,13 +504,14 @@ bool make_tmap_weights(CUtensorMap* map, const void* ptr, int tiled, uint64_t N,
 }
 
 // 3-D bf16 tensor map over a row-major [d2][d1][d0] array with a box of
-// b0 x b1 x b2 elements (b0 * 2 bytes = 128) and 128-byte swizzling.
+// b0 x b1 x b2 elements (b0 * 2 bytes = 128) and 128-byte swizzling; stride2:
+// elements from one d2 index to the next (0: d0 * d1).
 bool make_tmap_bf16_3d(CUtensorMap* map, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0,
-                       uint32_t b1, uint32_t b2) {
+                       uint32_t b1, uint32_t b2, uint64_t stride2) {
   auto enc = get_encode_fn();
   if (!enc) return false;
   cuuint64_t dims[3] = {d0, d1, d2};
-  cuuint64_t strides[2] = {d0 * 2, d0 * d1 * 2};
+  cuuint64_t strides[2] = {d0 * 2, (stride2 ? stride2 : d0 * d1) * 2};
   cuuint32_t box[3] = {b0, b1, b2};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,

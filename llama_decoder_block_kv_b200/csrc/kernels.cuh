@@ -85,7 +85,7 @@ int set_gemv_mma(int mode);
 // gemm_tc.cu
 bool make_tmap_bf16(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows);
 bool make_tmap_bf16_3d(CUtensorMap* map, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b0,
-                       uint32_t b1, uint32_t b2);
+                       uint32_t b1, uint32_t b2, uint64_t stride2 = 0);
 bool make_tmap_weights(CUtensorMap* map, const void* ptr, int tiled, uint64_t N, uint64_t K, uint32_t box_rows);
 // Scratch of the CTA-pair GEMM's two-way k split, for up to `tiles` 256 x 256
 // tiles: ws gemm_split_ws_floats(tiles) floats, sync gemm_split_sync_ints(tiles)
@@ -218,31 +218,13 @@ struct RaggedAttnParams {
   int* status;
 };
 
-// Request b's new tokens and keys, from device memory, with the checks of the
-// header: false (and the position range flag) for a request that is skipped.
-struct RaggedSeq {
-  int q0, n_new, kv;  // first row, new tokens, keys
-};
-__device__ __forceinline__ bool ragged_seq(const RaggedAttnParams& p, int b, RaggedSeq& s, bool flag) {
-  const int c0 = p.cu[b], c1 = p.cu[b + 1];
-  s.q0 = c0;
-  s.n_new = c1 - c0;
-  bool ok = c0 >= 0 && c1 >= c0 && c1 <= p.N && s.n_new <= p.max_new;
-  s.kv = ok ? s.n_new : 0;
-  if (p.tables && ok) {
-    s.kv = p.kv_lens[b];
-    ok = s.kv >= 0 && s.kv <= (p.max_pages << p.page_shift);
-  }
-  if (!ok) {
-    s.n_new = s.kv = 0;
-    if (flag) atomicOr(p.status, LLAMA_DEV_POS_RANGE);
-  }
-  return ok;
-}
-
 // attn_ragged.cu
 template <typename T>
 cudaError_t launch_attn_ragged_rows(const RaggedAttnParams& p, cudaStream_t st);
+// attn_ragged_tc.cu (bf16): partials of RAGGED_TC_CTAS CTAs and one counter each, zeroed once
+constexpr int RAGGED_TC_CTAS = 148;  // at most this many CTAs: one per SM
+size_t ragged_tc_ws_floats(int D);
+cudaError_t launch_attn_ragged_tc(const RaggedAttnParams& p, float* part, int* counters, int num_sms, cudaStream_t st);
 
 // decode_block.cu: one decode step of a whole block in one persistent launch
 constexpr int DB_RING_STAGES = 9;                 // 16 KB weight tiles in flight per SM

@@ -33,8 +33,32 @@ bool stride_ok(int64_t stride, int64_t width, int esz) {
 
 int launched(cudaError_t e) { return e == cudaSuccess ? LLAMA_OK : LLAMA_ERR_CUDA; }
 
-int attn(const RaggedAttnParams& p, int dtype, cudaStream_t st) {
-  return launched(dtype == LLAMA_BF16 ? launch_attn_ragged_rows<bf16>(p, st) : launch_attn_ragged_rows<float>(p, st));
+// SMs of the current device (asked once per device)
+int sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// Workspace: counters, then partials.
+constexpr size_t WS_COUNTERS = 4096;
+static_assert(RAGGED_TC_CTAS * sizeof(int) <= WS_COUNTERS, "counters");
+
+size_t ws_bytes(int dtype, int D) {
+  return WS_COUNTERS + (dtype == LLAMA_BF16 ? ragged_tc_ws_floats(D) * sizeof(float) : 0);
+}
+
+int attn(const RaggedAttnParams& p, int dtype, void* workspace, cudaStream_t st) {
+  const int sms = sm_count();
+  if (sms <= 0) return LLAMA_ERR_CUDA;
+  int* counters = static_cast<int*>(workspace);
+  float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + WS_COUNTERS);
+  if (dtype == LLAMA_BF16) return launched(launch_attn_ragged_tc(p, part, counters, sms, st));
+  return launched(launch_attn_ragged_rows<float>(p, st));
 }
 
 }  // namespace
@@ -102,7 +126,7 @@ int llama_rope_append(const llama_page_args* a, const void* qkv, int64_t qkv_str
 
 int64_t llama_attn_workspace_bytes(int dtype, int n_heads, int n_kv_heads, int head_dim) {
   if (!heads_ok(dtype, n_heads, n_kv_heads, head_dim)) return LLAMA_ERR_INVALID_ARGS;
-  return 256;
+  return (int64_t)ws_bytes(dtype, head_dim);
 }
 
 int llama_attn_paged(const llama_page_args* a, const void* q, int64_t q_stride, const void* k_pages,
@@ -136,7 +160,7 @@ int llama_attn_paged(const llama_page_args* a, const void* q, int64_t q_stride, 
   p.max_pages = a->max_pages;
   p.o = out;
   p.status = status;
-  return attn(p, a->dtype, reinterpret_cast<cudaStream_t>(stream));
+  return attn(p, a->dtype, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int llama_attn_packed(int dtype, int n_heads, int n_kv_heads, int head_dim, const void* q, int64_t q_stride,
@@ -170,7 +194,7 @@ int llama_attn_packed(int dtype, int n_heads, int n_kv_heads, int head_dim, cons
   p.D = head_dim;
   p.o = out;
   p.status = status;
-  return attn(p, dtype, reinterpret_cast<cudaStream_t>(stream));
+  return attn(p, dtype, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int llama_paged_status(int32_t* status, int* flags) {
