@@ -44,12 +44,25 @@
 namespace llama {
 
 namespace {
-constexpr int RT_KT = 128;  // keys per tile
+constexpr int RT_KT = 128;  // keys per tile (a K or V stage)
+constexpr int RT_UNIT = 1;  // what a unit costs besides its tiles, in tiles
 constexpr int RT_THREADS = 384;
+constexpr int RT_SEGS = 3;  // segments queued ahead
 constexpr int RT_LEADER = 128;  // first softmax thread
 constexpr float RT_LOG2E = 1.4426950408889634f;
 constexpr float RT_RESCALE = 8.0f;  // raise the running maximum only past 2^8
 }  // namespace
+
+// A segment: key tiles [j0, j1) of a unit (j1 = 0: the CTA's range ends here).
+struct RtSeg {
+  int b;                // request
+  RaggedSeq s;
+  int tok0, kvh, h0;    // first token and head of the unit's rows
+  int j0, j1, whole;    // whole: all of the unit's key tiles
+  int lim[2];           // key tiles that tiles A, B need (0 where the unit has no rows for B)
+  int slot;             // where a partial of it goes
+  int c0, c1, slot0;    // CTAs that share the unit, the slot of c0's partial
+};
 
 template <int D>
 struct RtCfg {
@@ -58,8 +71,8 @@ struct RtCfg {
   static constexpr uint32_t TILE = HALVES * HALF;        // a Q tile or a K or V stage
   static constexpr int STAGES = 131072 / TILE;           // 128 KB of ring
   static constexpr uint32_t S_COL = 0, O_COL = 256;      // S/P of A, B at 0, 128; O of A, B at 256, 384
-  static constexpr int BARS = 2 * STAGES + 10;
-  static constexpr size_t SMEM = 1024 + 2 * TILE + STAGES * TILE + BARS * 8 + 16;
+  static constexpr int BARS = 2 * STAGES + 21 + 2 * RT_SEGS;
+  static constexpr size_t SMEM = 1024 + 2 * TILE + STAGES * TILE + BARS * 8 + 16 + RT_SEGS * sizeof(RtSeg) + 8 + (RT_THREADS + 1) * 8;
 };
 
 // ---- the list of tiles
@@ -86,52 +99,87 @@ __host__ __device__ __forceinline__ long long rt_before(int c, int bq, long long
 __host__ __device__ __forceinline__ long long rt_total(int c, int n_new, int bq) {
   if (n_new <= 0) return 0;
   const int nt = (n_new + bq - 1) / bq;
-  return rt_before(c, bq, nt - 1) + rt_tiles(c, n_new, bq, nt - 1);
+  return rt_before(c, bq, nt - 1) + rt_tiles(c, n_new, bq, nt - 1) + (long long)RT_UNIT * nt;
 }
 __host__ __device__ __forceinline__ long long rt_begin(long long c, long long W, long long G) { return c * W / G; }
 __host__ __device__ __forceinline__ long long rt_own(long long x, long long W, long long G) { return ((x + 1) * G - 1) / W; }
 
-struct RtUnit {
+// A CTA's walk over its range [x, end) of the list. A unit stands there as RT_UNIT
+// + n entries: what it costs before its first tile, then its n key tiles.
+struct RtWalk {
+  long long x, end;
   int b, zl, t;  // request, (kv head, head group), q tile
   RaggedSeq s;
-  int c, nt;     // keys before the new tokens, q tiles
+  int c, nt;       // keys before the new tokens, q tiles
+  long long off;   // entries of the unit before x
+  // the current segment: key tiles [j0, j1) of n; key tiles that A and B need
+  // (0 where the unit has no rows for B); the unit's first entry
+  int j0, j1, n, lim[2];
+  long long xs;
 };
 
-__device__ __forceinline__ void rt_load(const RaggedAttnParams& p, int bq, RtUnit& u) {
-  ragged_seq(p, u.b, u.s, false);
-  u.c = max(u.s.kv - u.s.n_new, 0);
-  u.nt = (u.s.n_new + bq - 1) / bq;
+__device__ __forceinline__ void rt_load(const RaggedAttnParams& p, int bq, RtWalk& w) {
+  ragged_seq(p, w.b, w.s, false);
+  w.c = max(w.s.kv - w.s.n_new, 0);
+  w.nt = (w.s.n_new + bq - 1) / bq;
 }
-// pre[b]: tiles of one head group of the requests before b
-__device__ __forceinline__ int rt_locate(const RaggedAttnParams& p, const long long* pre, int HG, int bq, long long x,
-                                         RtUnit& u) {
-  int lo = 0, hi = p.B - 1;  // the last b whose tiles begin at or before x
+// to entry w.x; pre[i]: entries of one head group of the requests before i * per
+__device__ __forceinline__ void rt_start(const RaggedAttnParams& p, const long long* pre, int HG, int bq, RtWalk& w) {
+  if (w.x >= w.end) return;
+  int lo = 0, hi = RT_THREADS - 1;  // the last i whose entries begin at or before x
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] * HG <= x) lo = mid; else hi = mid - 1;
+    if (pre[mid] * HG <= w.x) lo = mid; else hi = mid - 1;
   }
-  u.b = lo;
-  rt_load(p, bq, u);
-  const long long per = pre[lo + 1] - pre[lo];
-  long long off = x - pre[lo] * HG;
-  u.zl = (int)(off / per);
-  off -= u.zl * per;
-  int a = 0, z = u.nt - 1;
+  long long off = w.x - pre[lo] * HG, per = 0;
+  for (w.b = lo * ((p.B + RT_THREADS - 1) / RT_THREADS);; ++w.b) {
+    rt_load(p, bq, w);
+    per = rt_total(w.c, w.s.n_new, bq);
+    if (off < per * HG || w.b == p.B - 1) break;
+    off -= per * HG;
+  }
+  w.zl = (int)(off / per);
+  off -= w.zl * per;
+  int a = 0, z = w.nt - 1;
   while (a < z) {
     const int mid = (a + z + 1) >> 1;
-    if (rt_before(u.c, bq, mid) <= off) a = mid; else z = mid - 1;
+    if (rt_before(w.c, bq, mid) + (long long)RT_UNIT * mid <= off) a = mid; else z = mid - 1;
   }
-  u.t = a;
-  return (int)(off - rt_before(u.c, bq, a));
+  w.t = a;
+  w.off = off - rt_before(w.c, bq, a) - (long long)RT_UNIT * a;
 }
-__device__ __forceinline__ void rt_next(const RaggedAttnParams& p, const long long* pre, int HG, int bq, RtUnit& u) {
-  if (++u.t < u.nt) return;
-  u.t = 0;
-  if (++u.zl < HG) return;
-  u.zl = 0;
-  do ++u.b;
-  while (u.b < p.B - 1 && pre[u.b + 1] == pre[u.b]);
-  rt_load(p, bq, u);
+// the next segment with tiles; false at the end of the range
+__device__ __forceinline__ bool rt_segment(int bq, RtWalk& w) {
+  while (w.x < w.end) {
+    w.n = rt_tiles(w.c, w.s.n_new, bq, w.t);
+    const long long take = min(RT_UNIT + w.n - w.off, w.end - w.x);
+    w.xs = w.x - w.off;
+    w.j0 = (int)max(w.off - RT_UNIT, 0LL);
+    w.j1 = (int)max(w.off + take - RT_UNIT, 0LL);
+    w.x += take;
+    w.off += take;
+    if (w.j1 > w.j0) {
+      const int bh = bq / 2, left = w.s.n_new - w.t * bq;
+      const long long first = (long long)w.c + (long long)w.t * bq + RT_KT - 1;
+      w.lim[0] = (int)((first + min(left, bh)) / RT_KT);
+      w.lim[1] = left > bh ? (int)((first + min(left, bq)) / RT_KT) : 0;
+      return true;
+    }
+  }
+  return false;
+}
+// on to the next unit, where the segment ended its unit
+__device__ __forceinline__ void rt_advance(const RaggedAttnParams& p, int HG, int bq, RtWalk& w) {
+  if (w.x >= w.end) return;
+  w.off = 0;
+  if (++w.t < w.nt) return;
+  w.t = 0;
+  if (++w.zl < HG) return;
+  w.zl = 0;
+  do {
+    ++w.b;
+    rt_load(p, bq, w);
+  } while (w.b < p.B - 1 && w.s.n_new == 0);
 }
 
 // ---- tensor-core and TMEM forms
@@ -174,7 +222,13 @@ __device__ __forceinline__ void rt_ld32(uint32_t taddr, float* v) {
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void rt_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// the N values that loads have been issued for are in (no use of them moves ahead of this)
+template <int N>
+__device__ __forceinline__ void rt_ld_wait(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
 __device__ __forceinline__ void rt_st32(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -184,6 +238,14 @@ __device__ __forceinline__ void rt_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void rt_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void rt_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -206,9 +268,14 @@ __device__ __forceinline__ uint64_t rt_add2(uint64_t a, uint64_t b) {
   asm("add.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-__device__ __forceinline__ float rt_max3(float a, float b, float c) {
+__device__ __forceinline__ float rt_max3(float a, float b, float c) {  // NaN where one is
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float rt_max2(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
 __device__ __forceinline__ float rt_ex2(float x) {  // 2^x on the special-function unit; -inf gives 0
@@ -233,14 +300,20 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
   uint64_t* kv_empty = kv_full + ST;   // [ST]
   uint64_t* q_full = kv_empty + ST;    // the segment's Q is in
   uint64_t* q_empty = q_full + 1;      // its last S has finished
-  uint64_t* s_full = q_empty + 1;      // [2] S of tile A / B written (and every MMA before it finished)
-  uint64_t* p_full = s_full + 2;       // [2] P written over S
-  uint64_t* o_full = p_full + 2;       // [2] the segment's last P V has finished
-  uint64_t* o_free = o_full + 2;       // [2] O has been read
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_free + 2);
+  uint64_t* s_full = q_empty + 1;      // [g] S of tile A / B written (and every MMA of it before that finished)
+  uint64_t* p_full = s_full + 2;       // [2 g + part] P of the first 96 / last 32 keys written over S
+  uint64_t* o_full = p_full + 4;       // [g] the segment's last P V has finished
+  uint64_t* o_free = o_full + 2;       // [g] O has been read
+  uint64_t* turn = o_free + 2;         // [4 g + quarter] the other tile's warp has taken its exponentials
+  uint64_t* g_full = turn + 8;         // [RT_SEGS] segment k is described in segs[k % RT_SEGS]
+  uint64_t* g_empty = g_full + RT_SEGS;  // its readers (a warp each) have left it
+  uint64_t* meet = g_empty + RT_SEGS;  // the softmax warps, at a cut unit
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meet + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* s_last = reinterpret_cast<int*>(tmem_slot + 2);
-  long long* pre = reinterpret_cast<long long*>(tmem_slot + 4);  // [B + 1]
+  RtSeg* segs = reinterpret_cast<RtSeg*>(tmem_slot + 4);
+  // entries of one head group of the requests before i * per, per = ceil(B / RT_THREADS)
+  long long* pre = reinterpret_cast<long long*>((reinterpret_cast<uintptr_t>(segs + RT_SEGS) + 7) & ~uintptr_t(7));  // [RT_THREADS + 1]
   __shared__ long long s_w[RT_THREADS / 32];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -250,13 +323,19 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&kv_empty[i], 2);
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);
+    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 128);
+    for (int i = 0; i < 8; ++i) mbar_init(&turn[i], 32);
+    mbar_init(meet, 256);
+    for (int i = 0; i < RT_SEGS; ++i) {
+      mbar_init(&g_full[i], 1);
+      mbar_init(&g_empty[i], 11);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
       mbar_init(&o_full[i], 1);
       mbar_init(&o_free[i], 128);
     }
@@ -287,33 +366,21 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     __syncthreads();
     x -= sum;
     for (int w = 0; w < warp; ++w) x += s_w[w];
-    for (int b = b0; b < b1; ++b) {
-      pre[b] = x;
-      ragged_seq(p, b, s, false);
-      x += rt_total(max(s.kv - s.n_new, 0), s.n_new, bq);
-      if (b == p.B - 1) pre[p.B] = x;
-    }
+    pre[tid] = x;
+    if (tid == RT_THREADS - 1) pre[RT_THREADS] = x + sum;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const long long W = pre[p.B] * HG, G = min((long long)gridDim.x, W), cta = blockIdx.x;
-  const long long xbeg = cta < G ? rt_begin(cta, W, G) : 0, xend = cta < G ? rt_begin(cta + 1, W, G) : 0;
-
-  // A segment: key tiles [j0, j1) of unit u; tile A has work up to na, B up to nb
-  // (0 where the unit has no rows for B)
-  RtUnit u;
-  int j0 = 0;
-  if (xbeg < xend) j0 = rt_locate(p, pre, HG, bq, xbeg, u);
-  auto limits = [&](const RtUnit& v, int& na, int& nb) {
-    const int left = v.s.n_new - v.t * bq;
-    nb = left > bh ? rt_tiles(v.c, v.s.n_new, bq, v.t) : 0;
-    na = (int)((v.c + (long long)v.t * bq + min(left, bh) + RT_KT - 1) / RT_KT);
+  // segment k, or false at the end of the range (or after a timeout); given back by leave()
+  auto enter = [&](int k) {
+    return wait_or_abort(&g_full[k % RT_SEGS], (k / RT_SEGS) & 1, p.status, abort_flag) && segs[k % RT_SEGS].j1 > 0;
   };
+  auto leave = [&](int k) { mbar_arrive(&g_empty[k % RT_SEGS]); };
 
   // 168 registers a thread at launch; the softmax threads hold a row of S and take
-  // what the first four warps (two of them idle) give back: 88 + 2 x 208 = 3 x 168
+  // what the first four warps give back: 88 + 2 x 208 = 3 x 168
   if (warp < 4) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == 0) {
@@ -325,34 +392,33 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     }
     int i = 0, seg = 0;
     bool ok = true;
-    for (long long x = xbeg; ok && x < xend; ++seg) {
-      const int n_u = rt_tiles(u.c, u.s.n_new, bq, u.t);
-      const int j1 = (int)min((long long)n_u, j0 + (xend - x));
-      int na, nb;
-      limits(u, na, nb);
-      const int kvh = u.zl / groups, h0 = kvh * n_rep + (u.zl - kvh * groups) * hpc;
+    while (ok && __all_sync(0xffffffffu, enter(seg))) {
+      const RtSeg& w = segs[seg % RT_SEGS];
+      const int kvh = w.kvh;
       if (lane == 0) {
         ok = wait_or_abort(q_empty, (seg & 1) ^ 1, p.status, abort_flag);
         if (ok) {
-          mbar_arrive_expect_tx(q_full, (nb ? 2 : 1) * Cfg::TILE);
-          for (int g = 0; g < (nb ? 2 : 1); ++g)
+          const int tiles = w.lim[1] ? 2 : 1;
+          mbar_arrive_expect_tx(q_full, tiles * Cfg::TILE);
+          for (int g = 0; g < tiles; ++g)
 #pragma unroll
             for (int hf = 0; hf < Cfg::HALVES; ++hf)
-              rt_tma_3d(sQ + g * Cfg::TILE + hf * Cfg::HALF, &map_q, q_full, hf * 64, h0, u.s.q0 + u.t * bq + g * bh);
+              rt_tma_3d(sQ + g * Cfg::TILE + hf * Cfg::HALF, &map_q, q_full, hf * 64, w.h0,
+                        w.s.q0 + w.tok0 + g * bh);
         }
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0);
       // lane -> (64-wide half, page of the tile); one box per lane
       const int ps = PAGED ? 1 << p.page_shift : RT_KT, boxes = Cfg::HALVES * (RT_KT / ps);
       const int hf = lane % Cfg::HALVES, pg = lane / Cfg::HALVES;
-      const int n_pages = PAGED ? (u.s.kv + ps - 1) >> p.page_shift : 0;
-      for (int j = j0; ok && j < j1; ++j) {
+      const int n_pages = PAGED ? (w.s.kv + ps - 1) >> p.page_shift : 0;
+      for (int j = w.j0; ok && j < w.j1; ++j) {
         int row = 0;
         if (PAGED && lane < boxes) {
           const int k = j * (RT_KT / ps) + pg;
           row = p.num_pages * p.Hkv * ps;  // out of range: zeros
           if (k < n_pages) {
-            const int page = __ldg(p.tables + (size_t)u.b * p.max_pages + k);
+            const int page = __ldg(p.tables + (size_t)w.b * p.max_pages + k);
             if ((unsigned)page < (unsigned)p.num_pages)
               row = (page * p.Hkv + kvh) * ps;
             else
@@ -373,32 +439,33 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
             if (PAGED)
               tma_load_2d(dst, map, &kv_full[st], hf * 64, row);
             else
-              rt_tma_3d(dst, map, &kv_full[st], hf * 64, kvh, u.s.q0 + j * RT_KT);
+              rt_tma_3d(dst, map, &kv_full[st], hf * 64, kvh, w.s.q0 + j * RT_KT);
           }
         }
       }
-      x += j1 - j0;
-      j0 = 0;
-      if (x < xend) rt_next(p, pre, HG, bq, u);
+      __syncwarp();
+      if (lane == 0) leave(seg);
+      ++seg;
     }
     // every copy lands before the CTA can retire
     if (lane == 0) {
       if (seg > 0) mbar_wait(q_full, (seg - 1) & 1, p.status);
       for (int k = (i > ST ? i - ST : 0); k < i; ++k) mbar_wait(&kv_full[k % ST], (k / ST) & 1, p.status);
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------------ MMA issuer
+  } else if (warp <= 2) {
+    if (elect_one()) {
+      // ------------------------------------------------------------------ MMA issuer of tile A / B
       constexpr uint32_t idesc_s = make_idesc_bf16(128, RT_KT);
       constexpr uint32_t idesc_pv = make_idesc_bf16(128, D) | (1u << 16);  // B (= V) N-major
-      int i = 0, seg = 0;
-      int pc[2] = {0, 0};  // P tiles taken of A, B
-      int oc[2] = {0, 0};  // segments with work of A, B
+      const int g = warp - 1;
+      const uint32_t qa = smem_u32(sQ + g * Cfg::TILE), kv = smem_u32(sKV);
+      const uint32_t sd = tmem + Cfg::S_COL + g * 128, od = tmem + Cfg::O_COL + g * 128;
+      int i = 0, seg = 0;     // ring slots, segments
+      int pc = 0, oc = 0;     // P tiles, segments with work
       bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t ph) { return ok = ok && wait_or_abort(bar, ph, p.status, abort_flag); };
-      auto issue_s = [&](int g, int slot) {
-        const uint32_t qa = smem_u32(sQ + g * Cfg::TILE), ka = smem_u32(sKV + (slot % ST) * Cfg::TILE);
-        const uint32_t sd = tmem + Cfg::S_COL + g * 128;
+      auto wait = [&](uint64_t* bar, uint32_t par) { return ok = ok && wait_or_abort(bar, par & 1, p.status, abort_flag); };
+      auto issue_s = [&](int st) {
+        const uint32_t ka = kv + st * Cfg::TILE;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * Cfg::HALF + (kk & 3) * 32;
@@ -406,50 +473,52 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
         }
         tc_commit(&s_full[g]);
       };
-      for (long long x = xbeg; ok && x < xend; ++seg) {
-        const int n_u = rt_tiles(u.c, u.s.n_new, bq, u.t);
-        const int j1 = (int)min((long long)n_u, j0 + (xend - x));
-        int lim[2];
-        limits(u, lim[0], lim[1]);
-        if (!wait(q_full, seg & 1) || !wait(&kv_full[i % ST], (i / ST) & 1)) break;
+      for (; ok && enter(seg); ++seg) {
+        const int j0 = segs[seg % RT_SEGS].j0, j1 = segs[seg % RT_SEGS].j1;
+        const int jl = min(j1, segs[seg % RT_SEGS].lim[g]);  // this tile has work on [j0, jl)
+        leave(seg);
+        if (!wait(q_full, seg) || !wait(&kv_full[i % ST], i / ST)) break;
         tc_fence_after();
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-          if (j0 < lim[g]) issue_s(g, i);
-        tc_commit(&kv_empty[i % ST]);
-        if (j1 - j0 == 1) tc_commit(q_empty);
-        for (int j = j0; ok && j < j1; ++j, i += 2) {
-          const int vs = i + 1, ks = i + 2;  // ring slots of V(j), K(j + 1)
-          if (!wait(&kv_full[vs % ST], (vs / ST) & 1)) break;
-          if (j + 1 < j1 && !wait(&kv_full[ks % ST], (ks / ST) & 1)) break;
-          const uint32_t va = smem_u32(sKV + (vs % ST) * Cfg::TILE);
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            if (j >= lim[g]) continue;
-            if (!wait(&p_full[g], pc[g] & 1)) break;
-            ++pc[g];
-            if (j == j0) {
-              if (!wait(&o_free[g], (oc[g] & 1) ^ 1)) break;
-              ++oc[g];
-            }
-            tc_fence_after();
-            const uint32_t od = tmem + Cfg::O_COL + g * 128, pa = tmem + Cfg::S_COL + g * 128;
-#pragma unroll
-            for (int kk = 0; kk < RT_KT / 16; ++kk)
-              rt_mma_ts(od, pa + kk * 8, rt_desc_n(va + kk * 2048, Cfg::HALF), idesc_pv, (j > j0 || kk > 0) ? 1u : 0u);
-            if (j + 1 < j1 && j + 1 < lim[g])
-              issue_s(g, ks);
-            else
-              tc_commit(&o_full[g]);
-          }
-          if (!ok) break;
-          tc_commit(&kv_empty[vs % ST]);
-          if (j + 1 < j1) tc_commit(&kv_empty[ks % ST]);
-          if (j + 2 == j1) tc_commit(q_empty);  // the segment's last S has been issued
+        if (j0 < jl) {
+          issue_s(i % ST);
+          tc_commit(&kv_empty[i % ST]);
+        } else {
+          mbar_arrive(&kv_empty[i % ST]);
         }
-        x += j1 - j0;
-        j0 = 0;
-        if (x < xend) rt_next(p, pre, HG, bq, u);
+        if (jl - j0 <= 1) tc_commit(q_empty);
+        for (int j = j0; j < j1; ++j, i += 2) {
+          const int vs = (i + 1) % ST, ks = (i + 2) % ST;  // ring stages of V(j), K(j + 1)
+          if (!wait(&kv_full[vs], (i + 1) / ST)) break;
+          if (j < jl) {
+            if (j == j0 && !wait(&o_free[g], oc++ ^ 1)) break;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (!wait(&p_full[2 * g + h], pc)) break;
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 6 * h; kk < 6 + 2 * h; ++kk)
+                rt_mma_ts(od, sd + kk * 8, rt_desc_n(kv + vs * Cfg::TILE + kk * 2048, Cfg::HALF), idesc_pv,
+                          (j > j0 || kk > 0) ? 1u : 0u);
+            }
+            if (!ok) break;
+            ++pc;
+            if (j + 1 == jl) tc_commit(&o_full[g]);
+          }
+          if (j + 1 < j1) {
+            if (!wait(&kv_full[ks], (i + 2) / ST)) break;
+            if (j + 1 < jl) {
+              issue_s(ks);
+              tc_commit(&kv_empty[ks]);
+            } else {
+              mbar_arrive(&kv_empty[ks]);
+            }
+          }
+          if (j < jl)
+            tc_commit(&kv_empty[vs]);
+          else
+            mbar_arrive(&kv_empty[vs]);
+          if (j + 2 == jl) tc_commit(q_empty);  // the segment's last S has been issued
+        }
       }
       // every MMA finishes before TMEM is freed: the softmax warps wait for all of
       // them (o_full), except after a timeout
@@ -459,6 +528,41 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
         while (global_timer_ns() - t0 < LLAMA_WAIT_LIMIT_NS / 16) {
         }
       }
+    }
+  } else if (lane == 0) {
+    // ------------------------------------------------------------------ scheduler
+    const long long W = pre[RT_THREADS] * HG, G = min((long long)gridDim.x, W), cta = blockIdx.x;
+    RtWalk w;
+    w.x = cta < G ? rt_begin(cta, W, G) : 0;
+    w.end = cta < G ? rt_begin(cta + 1, W, G) : 0;
+    const long long xbeg = w.x;
+    rt_start(p, pre, HG, bq, w);
+    for (int k = 0;; ++k) {
+      const bool more = rt_segment(bq, w);
+      if (!wait_or_abort(&g_empty[k % RT_SEGS], ((k / RT_SEGS) & 1) ^ 1, p.status, abort_flag)) break;
+      RtSeg& q = segs[k % RT_SEGS];
+      q.j1 = 0;
+      if (more) {
+        q.b = w.b;
+        q.s = w.s;
+        q.tok0 = w.t * bq;
+        q.kvh = w.zl / groups;
+        q.h0 = q.kvh * n_rep + (w.zl - q.kvh * groups) * hpc;
+        q.j0 = w.j0;
+        q.j1 = w.j1;
+        q.whole = w.j0 == 0 && w.j1 == w.n;
+        q.lim[0] = w.lim[0];
+        q.lim[1] = w.lim[1];
+        // a CTA has at most two cut units, one at either end of its range
+        q.slot = (int)(2 * cta + (w.xs <= xbeg ? 0 : 1));
+        const long long x0 = w.xs + RT_UNIT;  // the unit's first tile
+        q.c0 = (int)rt_own(x0, W, G);
+        q.c1 = (int)rt_own(x0 + w.n - 1, W, G);
+        q.slot0 = 2 * q.c0 + (w.xs <= rt_begin(q.c0, W, G) ? 0 : 1);
+      }
+      mbar_arrive(&g_full[k % RT_SEGS]);
+      if (!more) break;
+      rt_advance(p, HG, bq, w);
     }
   }
   } else {
@@ -472,120 +576,154 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     const uint64_t scale2 = rt_f2(sl2, sl2);
     const int pos_l = r / hpc, hl = r - pos_l * hpc;
     const int stride = 256 * D + 512;  // floats of one partial
-    int tiles = 0;                     // key tiles walked (ring slots 2 tiles, 2 tiles + 1)
     int sc = 0, oc = 0;                // S tiles taken, segments with work
+    int n = 0;                         // key tiles walked (ring slots 2 n, 2 n + 1)
     bool ok = true;
-    for (long long x = xbeg; x < xend;) {
-      const int n_u = rt_tiles(u.c, u.s.n_new, bq, u.t);
-      const int j1 = (int)min((long long)n_u, j0 + (xend - x));
-      int lim[2];
-      limits(u, lim[0], lim[1]);
-      const int jl = min(j1, lim[g]);  // this tile's rows have work on [j0, jl)
-      const int tok = u.t * bq + g * bh + pos_l;
+    // The warps of A and B on one scheduler take their exponentials in turn: A's tile
+    // n after B's n - 1, B's n after A's n. Left alone they fall into step, both at the
+    // exponentials and then both waiting for the tensor core.
+    auto my_turn = [&] {
+      if (g == 1 || n > 0) ok = wait_or_abort(&turn[4 * g + quarter], (g == 1 ? n : n - 1) & 1, p.status, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    int met = 0;
+    auto meet_all = [&] {
+      mbar_arrive(meet);
+      ok = wait_or_abort(meet, met++ & 1, p.status, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    auto pass_turn = [&] {
+      mbar_arrive(&turn[4 * (g ^ 1) + quarter]);
+      ++n;
+    };
+    for (int seg = 0; __all_sync(0xffffffffu, enter(seg)); ++seg) {
+      const RtSeg& w = segs[seg % RT_SEGS];
+      const int lim = w.lim[g], j1 = w.j1, jl = min(j1, lim);  // this tile's rows have work on [j0, jl)
+      const int tok = w.tok0 + g * bh + pos_l, kv_len = w.s.kv;
       // last key this row sees (rows past the last token follow it)
-      const int last = min(u.s.kv - u.s.n_new + min(tok, u.s.n_new - 1), u.s.kv - 1);
-      const bool live = __any_sync(0xffffffffu, tok < u.s.n_new);  // else no row of this warp is anyone's
+      const int last = min(w.s.kv - w.s.n_new + min(tok, w.s.n_new - 1), w.s.kv - 1);
+      const bool live = __any_sync(0xffffffffu, tok < w.s.n_new);  // else no row of this warp is anyone's
       float m_used = -INFINITY, l = 0.f;
-      for (int j = j0; ok && j < jl; ++j, ++sc) {
+      for (int j = w.j0; ok && j < j1; ++j) {
+        if (j >= jl) {
+          my_turn();
+          pass_turn();
+          continue;
+        }
         ok = wait_or_abort(&s_full[g], sc & 1, p.status, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        ++sc;
         tc_fence_after();
         const int key0 = j * RT_KT;
-        if (live) {
-        float s[RT_KT];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) rt_ld32(s_cols + 32 * c, s + 32 * c);
-        rt_ld_wait();
-        if (__any_sync(0xffffffffu, key0 + RT_KT - 1 > last)) {
-#pragma unroll
-          for (int c = 0; c < RT_KT; ++c)
-            if (key0 + c > last) s[c] = -INFINITY;
-        }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int c = 4; c < RT_KT - 4; c += 8)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = rt_max3(mx[e], s[c + 2 * e], s[c + 2 * e + 1]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[RT_KT - 4 + e]);
-        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;  // log2 units
-        if (j == j0) {
-          m_used = mt;
-        } else if (__any_sync(0xffffffffu, mt > m_used + RT_RESCALE)) {
-          // S(j) was issued behind P(j - 1) V(j - 1), so O is at rest
-          const float m_new = fmaxf(m_used, mt);
-          const float alpha = m_new == -INFINITY ? 1.f : rt_ex2(m_used - m_new);
-          l *= alpha;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float ov[32];
-            rt_ld32(o_cols + c, ov);
-            rt_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-            rt_st32(o_cols + c, reinterpret_cast<const uint32_t*>(ov));
-          }
-          m_used = m_new;
-        }
-        // p = 2^(s log2(e) / sqrt(D) - m) -> bf16 pairs over this row's S
-        const float m_ref = m_used == -INFINITY ? 0.f : m_used;
-        const uint64_t negm2 = rt_f2(-m_ref, -m_ref);
-        uint64_t ls[2] = {rt_f2(0.f, 0.f), rt_f2(0.f, 0.f)};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t ph[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            float t0, t1;
-            rt_split(rt_fma2(rt_f2(s[64 * h + 2 * e], s[64 * h + 2 * e + 1]), scale2, negm2), t0, t1);
-            const float p0 = rt_ex2(t0), p1 = rt_ex2(t1);
-            ls[e & 1] = rt_add2(ls[e & 1], rt_f2(p0, p1));
-            ph[e] = pack_bf16x2(p0, p1);
-          }
-          rt_st32(s_cols + 32 * h, ph);
-        }
-        float a0, a1, b0, b1;
-        rt_split(ls[0], a0, a1);
-        rt_split(ls[1], b0, b1);
-        l += (a0 + a1) + (b0 + b1);
-        }
-        if (key0 + RT_KT > u.s.kv) {
+        if (key0 + RT_KT > kv_len) {
           // V rows past the last key: zeros, before the MMA may read them
-          const int vs = 2 * (tiles + j - j0) + 1, row0 = max(u.s.kv - key0, 0);
+          const int vs = 2 * n + 1, row0 = max(kv_len - key0, 0);
           ok = wait_or_abort(&kv_full[vs % ST], (vs / ST) & 1, p.status, abort_flag);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          uint8_t* v = sKV + (vs % ST) * Cfg::TILE;
+          uint8_t* v = sKV + (vs % ST) * Cfg::TILE + row0 * 128;
           const int n16 = (RT_KT - row0) * 8;  // 16-byte pieces of one half
-          for (int e = r; e < n16 * Cfg::HALVES; e += 128)
-            *reinterpret_cast<uint4*>(v + (e / n16) * Cfg::HALF + row0 * 128 + (e % n16) * 16) = make_uint4(0, 0, 0, 0);
+          for (int k = r; k < n16 * Cfg::HALVES; k += 128)
+            *reinterpret_cast<uint4*>(v + (k / n16) * Cfg::HALF + (k % n16) * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
         }
-        rt_st_wait();
-        tc_fence_before();
-        mbar_arrive(&p_full[g]);
+        if (live) {
+          // p = 2^(s log2(e) / sqrt(D) - m) -> bf16 pairs over this row's S
+          float s[RT_KT];
+#pragma unroll
+          for (int c = 0; c < RT_KT; c += 32) rt_ld32(s_cols + c, s + c);
+          rt_ld_wait<RT_KT>(s);
+          if (__any_sync(0xffffffffu, key0 + RT_KT - 1 > last)) {
+#pragma unroll
+            for (int c = 0; c < RT_KT; ++c)
+              if (key0 + c > last) s[c] = -INFINITY;
+          }
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int c = 4; c < RT_KT - 4; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = rt_max3(mx[k], s[c + 2 * k], s[c + 2 * k + 1]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx[k] = rt_max2(mx[k], s[RT_KT - 4 + k]);
+          const float mt = rt_max3(rt_max2(mx[0], mx[1]), mx[2], mx[3]) * sl2;  // log2 units
+          if (j == w.j0) {
+            m_used = mt;
+          } else if (__any_sync(0xffffffffu, !(mt <= m_used + RT_RESCALE))) {
+            // S(j) was issued behind P(j - 1) V(j - 1), so O is at rest
+            const float m_new = rt_max2(m_used, mt);
+            const float alpha = m_new == -INFINITY ? 1.f : rt_ex2(m_used - m_new);
+            l *= alpha;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float ov[32];
+              rt_ld32(o_cols + c, ov);
+              rt_ld_wait<32>(ov);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) ov[k] *= alpha;
+              rt_st32(o_cols + c, reinterpret_cast<const uint32_t*>(ov));
+            }
+            m_used = m_new;
+          }
+          const float m_ref = m_used == -INFINITY ? 0.f : m_used;
+          const uint64_t negm2 = rt_f2(-m_ref, -m_ref);
+          uint64_t ls[2] = {rt_f2(0.f, 0.f), rt_f2(0.f, 0.f)};
+          auto weights = [&](int c0) {
+            uint32_t pp[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float p0, p1;
+              rt_split(rt_fma2(rt_f2(s[c0 + 2 * k], s[c0 + 2 * k + 1]), scale2, negm2), p0, p1);
+              p0 = rt_ex2(p0);
+              p1 = rt_ex2(p1);
+              ls[k & 1] = rt_add2(ls[k & 1], rt_f2(p0, p1));
+              pp[k] = pack_bf16x2(p0, p1);
+            }
+            rt_st16(s_cols + c0 / 2, pp);
+          };
+          my_turn();
+          if (!ok) break;
+          weights(0);
+          weights(32);
+          weights(64);
+          rt_st_wait();
+          tc_fence_before();
+          mbar_arrive(&p_full[2 * g]);
+          weights(96);
+          pass_turn();
+          float a0, a1, b0, b1;
+          rt_split(ls[0], a0, a1);
+          rt_split(ls[1], b0, b1);
+          l += (a0 + a1) + (b0 + b1);
+          rt_st_wait();
+          tc_fence_before();
+        } else {
+          my_turn();
+          pass_turn();
+          mbar_arrive(&p_full[2 * g]);
+        }
+        mbar_arrive(&p_full[2 * g + 1]);
       }
-      // after a timeout the warps still walk the segments, for the named barriers below
-      if (ok && j0 < jl) {
+      const bool work = w.j0 < jl;
+      if (ok && work) {
         ok = wait_or_abort(&o_full[g], oc & 1, p.status, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         ++oc;
         tc_fence_after();
       }
-      const bool work = ok && j0 < jl;
-      const int kvh = u.zl / groups, h = kvh * n_rep + (u.zl - kvh * groups) * hpc + hl;
-      const bool store = ok && tok < u.s.n_new && lim[g] > 0;
-      bf16* dst = reinterpret_cast<bf16*>(p.o) + ((size_t)(u.s.q0 + tok) * p.H + h) * D;
+      if (!ok) break;
+      const int h = w.h0 + hl;
+      const bool store = tok < w.s.n_new && lim > 0;
+      bf16* dst = reinterpret_cast<bf16*>(p.o) + ((size_t)(w.s.q0 + tok) * p.H + h) * D;
       bool bad = false;  // the row's result is not finite
-      if (j0 == 0 && j1 == n_u) {
+      if (w.whole) {
         const float inv = last < 0 ? 0.f : 1.f / l;  // a row without keys is zero
         if (work) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float ov[32];
             rt_ld32(o_cols + c, ov);
-            rt_ld_wait();
+            rt_ld_wait<32>(ov);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               ov[e] = last < 0 ? 0.f : ov[e] * inv;
@@ -601,15 +739,14 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
         bad = bad && store;
       } else {
         // partial: O as [D / 4][256 rows] float4, then (max, sum) per row
-        const long long xs = x - j0;  // the unit's first tile
-        float* pp = part + (size_t)(2 * cta + (xs <= xbeg ? 0 : 1)) * stride;
+        float* pp = part + (size_t)w.slot * stride;
         const int row = g * 128 + r;
         if (work) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float ov[32];
             rt_ld32(o_cols + c, ov);
-            rt_ld_wait();
+            rt_ld_wait<32>(ov);
             if (store)
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
@@ -620,21 +757,23 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
           mbar_arrive(&o_free[g]);
         }
         if (store) __stcg(reinterpret_cast<float2*>(pp + 256 * D) + row, make_float2(m_used, l));
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        const long long c0 = rt_own(xs, W, G), c1 = rt_own(xs + n_u - 1, W, G);
-        if (tid == RT_LEADER) *s_last = ok && atomic_add_acq_rel(&counters[c0], 1) == (int)(c1 - c0);
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        meet_all();
+        if (!ok) break;
+        const int c0 = w.c0, c1 = w.c1;
+        if (tid == RT_LEADER) *s_last = atomic_add_acq_rel(&counters[c0], 1) == c1 - c0;
+        meet_all();
+        if (!ok) break;
         if (*s_last) {
-          // partials of CTAs c0 .. c1 in that order; c0 holds the unit in its second
-          // slot unless its range starts at the unit, the others in their first
-          const long long slot0 = 2 * c0 + (rt_begin(c0, W, G) == xs ? 0 : 1);
+          // partials of CTAs c0 .. c1 in that order; c0 holds the unit in its second slot
+          // unless its range starts inside it, the others in their first
+          const int slot0 = w.slot0;
           if (store) {
             float mm = -INFINITY;
-            for (long long c = c0; c <= c1; ++c)
-              mm = fmaxf(mm, __ldcg(reinterpret_cast<const float2*>(part + (c == c0 ? slot0 : 2 * c) * stride + 256 * D) + row).x);
+            for (int c = c0; c <= c1; ++c)
+              mm = fmaxf(mm, __ldcg(reinterpret_cast<const float2*>(part + (size_t)(c == c0 ? slot0 : 2 * c) * stride + 256 * D) + row).x);
             float ll = 0.f;
-            for (long long c = c0; c <= c1; ++c) {
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + (c == c0 ? slot0 : 2 * c) * stride + 256 * D) + row);
+            for (int c = c0; c <= c1; ++c) {
+              const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + (size_t)(c == c0 ? slot0 : 2 * c) * stride + 256 * D) + row);
               if (ml.x != -INFINITY) ll += ml.y * rt_ex2(ml.x - mm);
             }
             const float inv = last < 0 ? 0.f : 1.f / ll;
@@ -643,8 +782,8 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
               float acc[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-              for (long long c = c0; c <= c1; ++c) {
-                const float* pc = part + (c == c0 ? slot0 : 2 * c) * stride;
+              for (int c = c0; c <= c1; ++c) {
+                const float* pc = part + (size_t)(c == c0 ? slot0 : 2 * c) * stride;
                 const float m_c = __ldcg(reinterpret_cast<const float2*>(pc + 256 * D) + row).x;
                 if (m_c == -INFINITY) continue;  // no weight there (and perhaps no O)
                 const float f = rt_ex2(m_c - mm);
@@ -668,16 +807,15 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
           }
           if (tid == RT_LEADER) counters[c0] = 0;  // re-armed for the next launch
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");  // s_last is written again by the next split segment
+        meet_all();  // s_last is written again by the next cut segment
+        if (!ok) break;
       }
       for (unsigned todo = __ballot_sync(0xffffffffu, bad); todo; todo &= todo - 1) {
         const int src = __ffs(todo) - 1;
-        ragged_row<bf16, D>(p, u.b, u.s, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, h, src), lane);
+        ragged_row<bf16, D>(p, w.b, w.s, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, h, src), lane);
       }
-      tiles += j1 - j0;
-      x += j1 - j0;
-      j0 = 0;
-      if (x < xend) rt_next(p, pre, HG, bq, u);
+      __syncwarp();
+      if (lane == 0) leave(seg);
     }
   }
 
@@ -704,10 +842,10 @@ template <int D, bool PAGED>
 static cudaError_t ragged_tc(const CUtensorMap* m, const RaggedAttnParams& p, float* part, int* counters, int grid,
                              int hpc, cudaStream_t st) {
   static std::atomic<unsigned long long> attr{0};
-  const size_t smem = RtCfg<D>::SMEM + (size_t)(LLAMA_MAX_SEQS + 1) * 8;
+  const size_t smem = RtCfg<D>::SMEM;
   cudaError_t e = ensure_smem(attn_ragged_tc_kernel<D, PAGED>, smem, attr);
   if (e != cudaSuccess) return e;
-  attn_ragged_tc_kernel<D, PAGED><<<grid, RT_THREADS, RtCfg<D>::SMEM + (size_t)(p.B + 1) * 8, st>>>(
+  attn_ragged_tc_kernel<D, PAGED><<<grid, RT_THREADS, smem, st>>>(
       m[0], m[1], m[2], p, part, counters, hpc);
   return cudaGetLastError();
 }
