@@ -48,6 +48,7 @@ constexpr int RT_KT = 128;  // keys per tile (a K or V stage)
 constexpr int RT_UNIT = 1;  // what a unit costs besides its tiles, in tiles
 constexpr int RT_THREADS = 384;
 constexpr int RT_SEGS = 3;  // segments queued ahead
+constexpr int RT_PRE = 128;  // prefix sums kept, at equal distances over the requests
 constexpr int RT_LEADER = 128;  // first softmax thread
 constexpr float RT_LOG2E = 1.4426950408889634f;
 constexpr float RT_RESCALE = 8.0f;  // raise the running maximum only past 2^8
@@ -72,7 +73,10 @@ struct RtCfg {
   static constexpr int STAGES = 131072 / TILE;           // 128 KB of ring
   static constexpr uint32_t S_COL = 0, O_COL = 256;      // S/P of A, B at 0, 128; O of A, B at 256, 384
   static constexpr int BARS = 2 * STAGES + 21 + 2 * RT_SEGS;
-  static constexpr size_t SMEM = 1024 + 2 * TILE + STAGES * TILE + BARS * 8 + 16 + RT_SEGS * sizeof(RtSeg) + 8 + (RT_THREADS + 1) * 8;
+  static constexpr uint32_t OUT = 4096;                  // a softmax warp's 32 rows x 64 bf16 on their way out
+  static constexpr size_t SMEM = 1024 + 2 * TILE + STAGES * TILE + 8 * OUT + BARS * 8 + 16 + RT_SEGS * sizeof(RtSeg) + 8 +
+                                 (RT_PRE + 1) * 8;
+  static_assert(SMEM + 256 <= 227 * 1024, "shared memory");
 };
 
 // ---- the list of tiles
@@ -126,13 +130,13 @@ __device__ __forceinline__ void rt_load(const RaggedAttnParams& p, int bq, RtWal
 // to entry w.x; pre[i]: entries of one head group of the requests before i * per
 __device__ __forceinline__ void rt_start(const RaggedAttnParams& p, const long long* pre, int HG, int bq, RtWalk& w) {
   if (w.x >= w.end) return;
-  int lo = 0, hi = RT_THREADS - 1;  // the last i whose entries begin at or before x
+  int lo = 0, hi = RT_PRE - 1;  // the last i whose entries begin at or before x
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (pre[mid] * HG <= w.x) lo = mid; else hi = mid - 1;
   }
   long long off = w.x - pre[lo] * HG, per = 0;
-  for (w.b = lo * ((p.B + RT_THREADS - 1) / RT_THREADS);; ++w.b) {
+  for (w.b = lo * ((p.B + RT_PRE - 1) / RT_PRE);; ++w.b) {
     rt_load(p, bq, w);
     per = rt_total(w.c, w.s.n_new, bq);
     if (off < per * HG || w.b == p.B - 1) break;
@@ -209,6 +213,16 @@ __device__ __forceinline__ void rt_tma_3d(void* dst, const CUtensorMap* map, uin
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+__device__ __forceinline__ void rt_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+// this thread's stores have read their shared memory / have finished
+__device__ __forceinline__ void rt_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void rt_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void rt_ld32(uint32_t taddr, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
@@ -287,7 +301,8 @@ __device__ __forceinline__ float rt_ex2(float x) {  // 2^x on the special-functi
 template <int D, bool PAGED>
 __global__ void __launch_bounds__(RT_THREADS, 1)
     attn_ragged_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                          const __grid_constant__ CUtensorMap map_v, const RaggedAttnParams p, float* __restrict__ part,
+                          const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_o,
+                          const RaggedAttnParams p, float* __restrict__ part,
                           int* __restrict__ counters, int hpc) {
   using Cfg = RtCfg<D>;
   constexpr int ST = Cfg::STAGES;
@@ -295,7 +310,8 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = base;
   uint8_t* sKV = sQ + 2 * Cfg::TILE;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + ST * Cfg::TILE);
+  uint8_t* sOut = sKV + ST * Cfg::TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + 8 * Cfg::OUT);
   uint64_t* kv_full = bars;            // [ST] stage i % ST holds the i-th of K(0), V(0), K(1), V(1), ...
   uint64_t* kv_empty = kv_full + ST;   // [ST]
   uint64_t* q_full = kv_empty + ST;    // the segment's Q is in
@@ -312,8 +328,8 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int* s_last = reinterpret_cast<int*>(tmem_slot + 2);
   RtSeg* segs = reinterpret_cast<RtSeg*>(tmem_slot + 4);
-  // entries of one head group of the requests before i * per, per = ceil(B / RT_THREADS)
-  long long* pre = reinterpret_cast<long long*>((reinterpret_cast<uintptr_t>(segs + RT_SEGS) + 7) & ~uintptr_t(7));  // [RT_THREADS + 1]
+  // entries of one head group of the requests before i * per, per = ceil(B / RT_PRE)
+  long long* pre = reinterpret_cast<long long*>((reinterpret_cast<uintptr_t>(segs + RT_SEGS) + 7) & ~uintptr_t(7));  // [RT_PRE + 1]
   __shared__ long long s_w[RT_THREADS / 32];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -348,7 +364,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
   }
   {
     // prefix sums of the requests' tiles
-    const int per = (p.B + RT_THREADS - 1) / RT_THREADS;
+    const int per = (p.B + RT_PRE - 1) / RT_PRE;  // the first RT_PRE threads take them
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     long long sum = 0;
     RaggedSeq s;
@@ -366,8 +382,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     __syncthreads();
     x -= sum;
     for (int w = 0; w < warp; ++w) x += s_w[w];
-    pre[tid] = x;
-    if (tid == RT_THREADS - 1) pre[RT_THREADS] = x + sum;
+    if (tid <= RT_PRE) pre[tid] = x;
   }
   tc_fence_before();
   __syncthreads();
@@ -531,7 +546,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     }
   } else if (lane == 0) {
     // ------------------------------------------------------------------ scheduler
-    const long long W = pre[RT_THREADS] * HG, G = min((long long)gridDim.x, W), cta = blockIdx.x;
+    const long long W = pre[RT_PRE] * HG, G = min((long long)gridDim.x, W), cta = blockIdx.x;
     RtWalk w;
     w.x = cta < G ? rt_begin(cta, W, G) : 0;
     w.end = cta < G ? rt_begin(cta + 1, W, G) : 0;
@@ -576,6 +591,8 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     const uint64_t scale2 = rt_f2(sl2, sl2);
     const int pos_l = r / hpc, hl = r - pos_l * hpc;
     const int stride = 256 * D + 512;  // floats of one partial
+    uint8_t* out = sOut + (warp - 4) * Cfg::OUT;
+    const int tok_end = 31 / hpc + quarter * 32 / hpc;  // the warp's last token, in the tile
     int sc = 0, oc = 0;                // S tiles taken, segments with work
     int n = 0;                         // key tiles walked (ring slots 2 n, 2 n + 1)
     bool ok = true;
@@ -718,7 +735,38 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
       bool bad = false;  // the row's result is not finite
       if (w.whole) {
         const float inv = last < 0 ? 0.f : 1.f / l;  // a row without keys is zero
-        if (work) {
+        // 32 rows of the request leave as boxes of 64 columns, by way of shared memory:
+        // a thread's stores to its own row touch a sector each
+        const bool boxes = w.tok0 + g * bh + tok_end < w.s.n_new;
+        if (work && boxes) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 64) {
+            float ov[64];
+            rt_ld32(o_cols + c, ov);
+            rt_ld32(o_cols + c + 32, ov + 32);
+            rt_ld_wait<64>(ov);
+            if (lane == 0) rt_store_wait_read();  // the box before has been read
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 64; ++e) {
+              ov[e] = last < 0 ? 0.f : ov[e] * inv;
+              bad |= !(fabsf(ov[e]) < INFINITY);
+            }
+#pragma unroll
+            for (int e = 0; e < 64; e += 8)
+              store8(reinterpret_cast<bf16*>(out + lane * 128 + (((e >> 3) ^ (lane & 7)) << 4)), ov + e);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+              rt_store_3d(&map_o, out, c, w.h0, w.s.q0 + w.tok0 + g * bh + tok_end - 31 / hpc);
+          }
+          tc_fence_before();
+          mbar_arrive(&o_free[g]);
+          if (__any_sync(0xffffffffu, bad)) {
+            if (lane == 0) rt_store_wait();  // before those rows are written again
+            __syncwarp();
+          }
+        } else if (work) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             float ov[32];
@@ -817,6 +865,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
       __syncwarp();
       if (lane == 0) leave(seg);
     }
+    if (lane == 0) rt_store_wait();
   }
 
   tc_fence_before();
@@ -846,14 +895,15 @@ static cudaError_t ragged_tc(const CUtensorMap* m, const RaggedAttnParams& p, fl
   cudaError_t e = ensure_smem(attn_ragged_tc_kernel<D, PAGED>, smem, attr);
   if (e != cudaSuccess) return e;
   attn_ragged_tc_kernel<D, PAGED><<<grid, RT_THREADS, smem, st>>>(
-      m[0], m[1], m[2], p, part, counters, hpc);
+      m[0], m[1], m[2], m[3], p, part, counters, hpc);
   return cudaGetLastError();
 }
 
 cudaError_t launch_attn_ragged_tc(const RaggedAttnParams& p, float* part, int* counters, int num_sms, cudaStream_t st) {
   const int hpc = prefill_heads_per_cta(p.H / p.Hkv);
-  CUtensorMap m[3];
-  bool ok = make_tmap_rows_bf16(&m[0], p.q, p.D, p.H, p.N, p.q_stride, hpc, 128 / hpc);
+  CUtensorMap m[4];
+  bool ok = make_tmap_rows_bf16(&m[0], p.q, p.D, p.H, p.N, p.q_stride, hpc, 128 / hpc) &&
+            make_tmap_rows_bf16(&m[3], p.o, p.D, p.H, p.N, (long long)p.H * p.D, hpc, 32 / hpc);
   if (p.tables) {
     const uint64_t rows = ((uint64_t)p.num_pages * p.Hkv) << p.page_shift;
     ok = ok && make_tmap_bf16(&m[1], p.k, rows, p.D, 1u << p.page_shift) &&
