@@ -225,6 +225,11 @@ cudaError_t launch_attn_ragged_rows(const RaggedAttnParams& p, cudaStream_t st);
 constexpr int RAGGED_TC_CTAS = 148;  // at most this many CTAs: one per SM
 size_t ragged_tc_ws_floats(int D);
 cudaError_t launch_attn_ragged_tc(const RaggedAttnParams& p, float* part, int* counters, int num_sms, cudaStream_t st);
+// attn_ragged_decode.cu (bf16, pages, at most one new token a request): the same of RAGGED_DECODE_CTAS CTAs
+constexpr int RAGGED_DECODE_CTAS = 296;  // at most this many CTAs: two per SM
+size_t ragged_decode_ws_floats(int D);
+cudaError_t launch_attn_ragged_decode(const RaggedAttnParams& p, float* part, int* counters, int num_sms,
+                                      cudaStream_t st);
 
 // decode_block.cu: one decode step of a whole block in one persistent launch
 constexpr int DB_RING_STAGES = 9;                 // 16 KB weight tiles in flight per SM
