@@ -352,9 +352,24 @@ class PageArgs:
         if self.dtype not in _TORCH:
             raise ValueError(f"dtype {self.dtype!r}: 'fp32' or 'bf16'")
 
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_ref", None)
+
+    def ref(self):
+        """Reference to the C structure, built once for these values."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = self.__dict__["_ref"] = ctypes.byref(self.c())
+        return r
+
     def c(self) -> LlamaPageArgs:
         return LlamaPageArgs(LLAMA_BF16 if self.dtype == "bf16" else LLAMA_FP32, self.n_heads, self.n_kv_heads,
                              self.head_dim, self.page_size, self.num_pages, self.max_pages)
+
+
+def _raw_stream(stream) -> int:
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def _on_device(name: str, t: torch.Tensor, dtype, device: int) -> int:
@@ -367,6 +382,8 @@ def _on_device(name: str, t: torch.Tensor, dtype, device: int) -> int:
 
 def _whole(name: str, t: torch.Tensor, dtype, shape, device: int) -> int:
     """Pointer of a contiguous tensor of this type and shape (-1: any extent)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()  # a call's time is mostly this on small steps
     p = _on_device(name, t, dtype, device)
     if len(t.shape) != len(shape) or any(w != -1 and n != w for n, w in zip(t.shape, shape)):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -377,8 +394,11 @@ def _whole(name: str, t: torch.Tensor, dtype, shape, device: int) -> int:
 
 def _rows(name: str, t: torch.Tensor, dtype, n: int, heads: int, head_dim: int, device: int):
     """Pointer and row stride of [n][heads][head_dim] rows that may stand apart (a slice of a wider matrix)."""
-    p = _on_device(name, t, dtype, device)
-    if tuple(t.shape) != (n, heads, head_dim):
+    if t.dtype is dtype and t.get_device() == device:
+        p = t.data_ptr()
+    else:
+        p = _on_device(name, t, dtype, device)
+    if t.shape != (n, heads, head_dim):
         raise ValueError(f"{name} must have shape {(n, heads, head_dim)}, got {tuple(t.shape)}")
     s0, s1, s2 = t.stride()
     if s2 != 1 or (heads > 1 and s1 != head_dim):
@@ -395,12 +415,12 @@ def llama_page_plan(args: PageArgs, cached_lens: torch.Tensor, new_lens: torch.T
     d, i32 = torch.cuda.current_device(), torch.int32
     n, T = cached_lens.shape[0], positions.shape[0]
     _check(lib().llama_page_plan(
-        ctypes.byref(args.c()), _whole("cached_lens", cached_lens, i32, (n,), d), _whole("new_lens", new_lens, i32, (n,), d),
+        args.ref(), _whole("cached_lens", cached_lens, i32, (n,), d), _whole("new_lens", new_lens, i32, (n,), d),
         n, T, _whole("block_tables", block_tables, i32, (n, args.max_pages), d),
         _whole("free_pages", free_pages, i32, (args.num_pages,), d), _whole("free_count", free_count, i32, (1,), d),
         _whole("free_count_out", free_count_out, i32, (1,), d), _whole("cu", cu, i32, (n + 1,), d),
         _whole("kv_lens", kv_lens, i32, (n,), d), _whole("positions", positions, i32, (T,), d),
-        _whole("slots", slots, i32, (T,), d), _whole("status", status, i32, (1,), d), _stream(stream)), "llama_page_plan")
+        _whole("slots", slots, i32, (T,), d), _whole("status", status, i32, (1,), d), _raw_stream(stream)), "llama_page_plan")
 
 
 def llama_rope_append(args: PageArgs, qkv: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
@@ -417,11 +437,11 @@ def llama_rope_append(args: PageArgs, qkv: torch.Tensor, positions: torch.Tensor
         raise ValueError(f"qkv must have shape (n, {width}) with contiguous rows, got {tuple(qkv.shape)}")
     pool = (args.num_pages, args.n_kv_heads, args.page_size, D)
     _check(lib().llama_rope_append(
-        ctypes.byref(args.c()), _on_device("qkv", qkv, qkv.dtype, d), qkv.stride(0) if n > 1 else width, _CODE[qkv.dtype],
+        args.ref(), _on_device("qkv", qkv, qkv.dtype, d), qkv.stride(0) if n > 1 else width, _CODE[qkv.dtype],
         _whole("positions", positions, i32, (n,), d), _whole("slots", slots, i32, (n,), d), n,
         _whole("rope", rope, torch.float32, (-1, D // 2, 2), d), rope.shape[0],
         _whole("q_out", q_out, dt, (n, args.n_heads, D), d), _whole("k_pages", k_pages, dt, pool, d),
-        _whole("v_pages", v_pages, dt, pool, d), _whole("status", status, i32, (1,), d), _stream(stream)),
+        _whole("v_pages", v_pages, dt, pool, d), _whole("status", status, i32, (1,), d), _raw_stream(stream)),
         "llama_rope_append")
 
 
@@ -442,11 +462,11 @@ def llama_attn_paged(args: PageArgs, q: torch.Tensor, k_pages: torch.Tensor, v_p
     pool = (args.num_pages, args.n_kv_heads, args.page_size, D)
     qp, qs = _rows("q", q, dt, n, args.n_heads, D, d)
     _check(lib().llama_attn_paged(
-        ctypes.byref(args.c()), qp, qs, _whole("k_pages", k_pages, dt, pool, d), _whole("v_pages", v_pages, dt, pool, d),
+        args.ref(), qp, qs, _whole("k_pages", k_pages, dt, pool, d), _whole("v_pages", v_pages, dt, pool, d),
         _whole("block_tables", block_tables, i32, (B, args.max_pages), d), _whole("cu", cu, i32, (B + 1,), d),
         _whole("kv_lens", kv_lens, i32, (B,), d), B, n, int(max_new), _whole("out", out, dt, (n, args.n_heads, D), d),
         _whole("workspace", workspace, torch.uint8, (-1,), d), workspace.shape[0],
-        _whole("status", status, i32, (1,), d), _stream(stream)), "llama_attn_paged")
+        _whole("status", status, i32, (1,), d), _raw_stream(stream)), "llama_attn_paged")
 
 
 def llama_attn_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, max_len: int,
@@ -464,7 +484,7 @@ def llama_attn_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: tor
     _check(lib().llama_attn_packed(
         _CODE[dt], H, Hkv, D, qp, qs, kp, ks, vp, vs, _whole("cu", cu, i32, (-1,), d), cu.shape[0] - 1, n, int(max_len),
         _whole("out", out, dt, (n, H, D), d), _whole("workspace", workspace, torch.uint8, (-1,), d), workspace.shape[0],
-        _whole("status", status, i32, (1,), d), _stream(stream)), "llama_attn_packed")
+        _whole("status", status, i32, (1,), d), _raw_stream(stream)), "llama_attn_packed")
 
 
 def llama_paged_status(status: torch.Tensor):

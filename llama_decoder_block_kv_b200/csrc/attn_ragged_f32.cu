@@ -1,0 +1,306 @@
+// Causal attention of packed rows over a paged cache or over packed keys, in fp32 on
+// the CUDA cores: softmax_j(q.k_j / sqrt(D)) V over the keys j <= p of each row.
+//
+// What bounds it: the FMA pipe where rows share their keys (2 D products per row and
+// key), HBM for single tokens. A unit is 32 query rows of one (request, kv head): hpc
+// query heads (the largest power of two up to 8 dividing n_rep) x 32 / hpc positions;
+// it walks 64-key tiles up to its last position. The tiles of all units form one list,
+// cut evenly over the CTAs (ragged.cuh), because fp32 models are small: a few short
+// prompts have fewer units than the GPU has SMs. A unit cut between CTAs leaves
+// partials (max, sum, O), merged in CTA order by the CTA that arrives last.
+//
+// 128 threads, thread (ty, tx) of 8 x 16: scores of rows 4 ty .. + 3 with keys tx + 16 k,
+// then outputs of the same rows with columns 4 tx .. + 3 (+ 64): each 16-byte read of
+// shared memory serves 8 products. K(j + 1) is copied while P(j) V(j) runs and V(j + 1)
+// while the scores of j + 1 are taken (cp.async; keys past the last one are zeros).
+//
+// A V row of a later key that is not finite reaches the earlier rows of its tile (0 x
+// NaN): rows whose result is not finite are computed again, key by key.
+#include "ragged.cuh"
+
+#include <algorithm>
+
+namespace llama {
+
+namespace {
+constexpr int RF_KT = 64;       // keys per tile
+constexpr int RF_ROWS = 32;     // query rows per unit
+constexpr int RF_THREADS = 128;
+constexpr float RF_LOG2E = 1.4426950408889634f;
+}  // namespace
+
+template <int D>
+struct RfCfg {
+  static constexpr int LD = D + 4;      // row stride of Q and K: 16 rows on distinct banks
+  static constexpr int LDP = RF_KT + 4;
+  static constexpr int FLOATS = RF_ROWS * LD + RF_KT * LD + RF_KT * D + RF_ROWS * LDP;
+  static constexpr size_t SMEM = FLOATS * 4;
+  static constexpr int PER_SM = D == 64 ? 4 : 2;  // resident CTAs (shared memory)
+};
+
+__device__ __forceinline__ void rf_copy16(void* dst, const void* src, int bytes) {  // bytes 0: zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void rf_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void rf_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+template <int D>
+__global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
+    attn_ragged_f32_kernel(const RaggedAttnParams p, float* __restrict__ part, int* __restrict__ counters, int hpc) {
+  using Cfg = RfCfg<D>;
+  constexpr int LD = Cfg::LD, LDP = Cfg::LDP, NC = D / 64;
+  extern __shared__ float4 rf_smem[];
+  float* sQ = reinterpret_cast<float*>(rf_smem);
+  float* sK = sQ + RF_ROWS * LD;
+  float* sV = sK + RF_KT * LD;
+  float* sP = sV + RF_KT * D;
+  __shared__ long long pre[RT_PRE + 1];
+  __shared__ long long s_w[RF_THREADS / 32];
+  __shared__ int s_last;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tx = tid & 15, ty = tid >> 4;
+  const int n_rep = p.H / p.Hkv, groups = n_rep / hpc, HG = p.Hkv * groups, bq = RF_ROWS / hpc;
+  const int stride = RF_ROWS * D + 2 * RF_ROWS;  // floats of one partial
+  const float sl2 = rsqrtf((float)D) * RF_LOG2E;
+  rt_prefix<RF_KT>(p, bq, pre, s_w);
+  const long long W = pre[RT_PRE] * HG, G = min((long long)gridDim.x, W), cta = blockIdx.x;
+  RtWalk w;
+  w.x = cta < G ? rt_begin(cta, W, G) : 0;
+  w.end = cta < G ? rt_begin(cta + 1, W, G) : 0;
+  const long long xbeg = w.x;
+  rt_start<RF_KT>(p, pre, HG, bq, w);
+  for (; rt_segment<RF_KT>(bq, w); rt_advance(p, HG, bq, w)) {
+    const int kvh = w.zl / groups, h0 = kvh * n_rep + (w.zl - kvh * groups) * hpc, tok0 = w.t * bq;
+    auto load = [&](float* dst, int ld, const void* src, long long row_stride, int j) {
+#pragma unroll 4
+      for (int e = tid; e < RF_KT * D / 4; e += RF_THREADS) {
+        const int r = e / (D / 4), c = (e - r * (D / 4)) * 4, key = j * RF_KT + r;
+        bool have = key < w.s.kv;
+        size_t at = 0;
+        if (p.tables) {
+          if (have) {
+            const int page = __ldg(p.tables + (size_t)w.b * p.max_pages + (key >> p.page_shift));
+            have = (unsigned)page < (unsigned)p.num_pages;
+            if (have)
+              at = (((((size_t)page * p.Hkv + kvh) << p.page_shift) + (key & ((1 << p.page_shift) - 1))) * D) + c;
+            else
+              atomicOr(p.status, LLAMA_DEV_PAGE_RANGE);
+          }
+        } else if (have) {
+          at = (size_t)(w.s.q0 + key) * row_stride + (size_t)kvh * D + c;
+        }
+        rf_copy16(dst + r * ld + c, static_cast<const float*>(src) + at, have ? 16 : 0);
+      }
+      rf_commit();
+    };
+    __syncthreads();  // shared memory of the segment before has been read
+    for (int e = tid; e < RF_ROWS * D / 4; e += RF_THREADS) {
+      const int r = e / (D / 4), c = (e - r * (D / 4)) * 4, tok = tok0 + r / hpc;
+      const bool have = tok < w.s.n_new;
+      const size_t at = have ? (size_t)(w.s.q0 + tok) * p.q_stride + (size_t)(h0 + r % hpc) * D + c : 0;
+      rf_copy16(sQ + r * LD + c, static_cast<const float*>(p.q) + at, have ? 16 : 0);
+    }
+    load(sK, LD, p.k, p.k_stride, w.j0);
+    load(sV, D, p.v, p.v_stride, w.j0);
+
+    const bool live = tok0 + 8 * warp / hpc < w.s.n_new;  // a row of this warp is someone's
+    int last[4];                                          // last key each row sees
+    float m[4], l[4], o[4][4 * NC];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = tok0 + (4 * ty + i) / hpc;
+      last[i] = min(w.s.kv - w.s.n_new + min(tok, w.s.n_new - 1), w.s.kv - 1);
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.f;
+    }
+    for (int j = w.j0; j < w.j1; ++j) {
+      rf_wait_but_one();
+      __syncthreads();  // Q, K(j) in; P(j - 1), V(j - 1) read
+      float s[4][4];
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+          float4 q[4], k[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(sQ + (4 * ty + i) * LD + d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) k[i] = *reinterpret_cast<const float4*>(sK + (tx + 16 * i) * LD + d);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              s[i][c] = fmaf(q[i].x, k[c].x, fmaf(q[i].y, k[c].y, fmaf(q[i].z, k[c].z, fmaf(q[i].w, k[c].w, s[i][c]))));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float mt = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            s[i][c] = j * RF_KT + tx + 16 * c > last[i] ? -INFINITY : s[i][c] * sl2;
+            mt = fmaxf(mt, s[i][c]);
+          }
+#pragma unroll
+          for (int x = 8; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
+          const float mn = fmaxf(m[i], mt), ref = mn == -INFINITY ? 0.f : mn, a = exp2f(m[i] - ref);
+          m[i] = mn;
+          float sum = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float e = exp2f(s[i][c] - ref);
+            sum += e;
+            sP[(4 * ty + i) * LDP + tx + 16 * c] = e;
+          }
+          l[i] = l[i] * a + sum;  // of this thread's keys
+#pragma unroll
+          for (int c = 0; c < 4 * NC; ++c) o[i][c] *= a;
+        }
+      }
+      __syncthreads();  // K(j) read
+      if (j + 1 < w.j1)
+        load(sK, LD, p.k, p.k_stride, j + 1);
+      else
+        rf_commit();
+      rf_wait_but_one();
+      __syncthreads();  // V(j), P(j) in
+      if (live) {
+#pragma unroll 4
+        for (int k = 0; k < RF_KT; k += 4) {
+          float4 pr[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) pr[i] = *reinterpret_cast<const float4*>(sP + (4 * ty + i) * LDP + k);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              const float4 v = *reinterpret_cast<const float4*>(sV + (k + kk) * D + 64 * c + 4 * tx);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float e = kk == 0 ? pr[i].x : kk == 1 ? pr[i].y : kk == 2 ? pr[i].z : pr[i].w;
+                o[i][4 * c] = fmaf(e, v.x, o[i][4 * c]);
+                o[i][4 * c + 1] = fmaf(e, v.y, o[i][4 * c + 1]);
+                o[i][4 * c + 2] = fmaf(e, v.z, o[i][4 * c + 2]);
+                o[i][4 * c + 3] = fmaf(e, v.w, o[i][4 * c + 3]);
+              }
+            }
+        }
+      }
+      __syncthreads();  // V(j) read
+      if (j + 1 < w.j1)
+        load(sV, D, p.v, p.v_stride, j + 1);
+      else
+        rf_commit();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+
+    bool bad[4] = {false, false, false, false};  // the row's result is not finite
+    // normalise and store row i of this thread (columns 4 tx + 64 c)
+    auto finish = [&](int i, float sum) {
+      const int r = 4 * ty + i, tok = tok0 + r / hpc;
+      if (tok >= w.s.n_new) return;
+      float* dst = static_cast<float*>(p.o) + ((size_t)(w.s.q0 + tok) * p.H + h0 + r % hpc) * D;
+      const float inv = 1.f / sum;
+#pragma unroll
+      for (int c = 0; c < 4 * NC; ++c) {
+        o[i][c] = last[i] < 0 ? 0.f : o[i][c] * inv;  // a row without keys is zero
+        bad[i] |= !(fabsf(o[i][c]) < INFINITY);
+      }
+#pragma unroll
+      for (int c = 0; c < NC; ++c) store4(dst + 64 * c + 4 * tx, o[i] + 4 * c);
+    };
+    if (w.j0 == 0 && w.j1 == w.n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) finish(i, l[i]);
+    } else {
+      // a CTA has at most two cut units, one at either end of its range
+      float* pp = part + (size_t)(2 * cta + (w.xs <= xbeg ? 0 : 1)) * stride;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 4 * ty + i;
+        if (tok0 + r / hpc >= w.s.n_new) continue;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+          __stcg(reinterpret_cast<float4*>(pp + r * D + 64 * c + 4 * tx),
+                 make_float4(o[i][4 * c], o[i][4 * c + 1], o[i][4 * c + 2], o[i][4 * c + 3]));
+        if (tx == 0) __stcg(reinterpret_cast<float2*>(pp + RF_ROWS * D) + r, make_float2(m[i], l[i]));
+      }
+      __syncthreads();
+      const long long x0 = w.xs + RT_UNIT;  // the unit's first tile
+      const int c0 = (int)rt_own(x0, W, G), c1 = (int)rt_own(x0 + w.n - 1, W, G);
+      if (tid == 0) s_last = atomic_add_acq_rel(&counters[c0], 1) == c1 - c0;
+      __syncthreads();
+      if (s_last) {
+        const int slot0 = 2 * c0 + (w.xs <= rt_begin(c0, W, G) ? 0 : 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 4 * ty + i;
+          if (tok0 + r / hpc >= w.s.n_new) continue;
+          float mm = -INFINITY, ll = 0.f;
+          for (int c = c0; c <= c1; ++c)
+            mm = fmaxf(mm, __ldcg(reinterpret_cast<const float2*>(part + (size_t)(c == c0 ? slot0 : 2 * c) * stride + RF_ROWS * D) + r).x);
+#pragma unroll
+          for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.f;
+          for (int c = c0; c <= c1; ++c) {
+            const float* pc = part + (size_t)(c == c0 ? slot0 : 2 * c) * stride;
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pc + RF_ROWS * D) + r);
+            if (ml.x == -INFINITY) continue;
+            const float f = exp2f(ml.x - mm);
+            ll += ml.y * f;
+#pragma unroll
+            for (int k = 0; k < NC; ++k) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(pc + r * D + 64 * k + 4 * tx));
+              o[i][4 * k] += v.x * f;
+              o[i][4 * k + 1] += v.y * f;
+              o[i][4 * k + 2] += v.z * f;
+              o[i][4 * k + 3] += v.w * f;
+            }
+          }
+          finish(i, ll);
+        }
+        if (tid == 0) counters[c0] = 0;  // re-armed for the next launch
+      }
+      __syncthreads();  // s_last is written again by the next cut segment
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const unsigned b = __ballot_sync(0xffffffffu, bad[i]);
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+        if ((b >> (16 * half)) & 0xffffu) {
+          __syncwarp();  // behind the stores above
+          const int r = 8 * warp + 4 * half + i;
+          ragged_row<float, D>(p, w.b, w.s, tok0 + r / hpc, h0 + r % hpc, lane);
+        }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ host side
+
+size_t ragged_f32_ws_floats(int D) {
+  return (size_t)2 * (D == 64 ? RAGGED_F32_CTAS : RAGGED_F32_CTAS / 2) * (RF_ROWS * D + 2 * RF_ROWS);
+}
+
+template <int D>
+static cudaError_t ragged_f32(const RaggedAttnParams& p, float* part, int* counters, int num_sms, cudaStream_t st) {
+  static std::atomic<unsigned long long> attr{0};
+  cudaError_t e = ensure_smem(attn_ragged_f32_kernel<D>, RfCfg<D>::SMEM, attr);
+  if (e != cudaSuccess) return e;
+  const int grid = std::min(num_sms, RAGGED_F32_CTAS / 4) * RfCfg<D>::PER_SM;
+  attn_ragged_f32_kernel<D><<<grid, RF_THREADS, RfCfg<D>::SMEM, st>>>(p, part, counters,
+                                                                      prefill_heads_per_cta(p.H / p.Hkv));
+  return cudaGetLastError();
+}
+
+cudaError_t launch_attn_ragged_f32(const RaggedAttnParams& p, float* part, int* counters, int num_sms,
+                                   cudaStream_t st) {
+  return p.D == 128 ? ragged_f32<128>(p, part, counters, num_sms, st) : ragged_f32<64>(p, part, counters, num_sms, st);
+}
+
+}  // namespace llama

@@ -45,10 +45,8 @@ namespace llama {
 
 namespace {
 constexpr int RT_KT = 128;  // keys per tile (a K or V stage)
-constexpr int RT_UNIT = 1;  // what a unit costs besides its tiles, in tiles
 constexpr int RT_THREADS = 384;
 constexpr int RT_SEGS = 3;  // segments queued ahead
-constexpr int RT_PRE = 128;  // prefix sums kept, at equal distances over the requests
 constexpr int RT_LEADER = 128;  // first softmax thread
 constexpr float RT_LOG2E = 1.4426950408889634f;
 constexpr float RT_RESCALE = 8.0f;  // raise the running maximum only past 2^8
@@ -78,113 +76,6 @@ struct RtCfg {
                                  (RT_PRE + 1) * 8;
   static_assert(SMEM + 256 <= 227 * 1024, "shared memory");
 };
-
-// ---- the list of tiles
-
-// q tile t of a request: its key tiles; the sum over the tiles before it (all full)
-__host__ __device__ __forceinline__ int rt_tiles(int c, int n_new, int bq, int t) {
-  const long long last = min((long long)(t + 1) * bq, (long long)n_new);
-  return (int)((c + last + RT_KT - 1) / RT_KT);
-}
-__host__ __device__ __forceinline__ long long rt_floor_sum(long long m, int r) {  // sum of i / r over i < m
-  const long long q = m / r;
-  return r * (q * (q - 1) / 2) + q * (m - q * r);
-}
-__host__ __device__ __forceinline__ long long rt_before(int c, int bq, long long t) {
-  if (bq >= RT_KT) {
-    const int s = bq / RT_KT;
-    return t * (((long long)c + RT_KT - 1) / RT_KT) + s * (t * (t + 1) / 2);
-  }
-  // ceil((c + (i + 1) bq) / 128) = floor((e + i) / r) + 1 with e = ceil(c / bq), r = 128 / bq
-  const int r = RT_KT / bq;
-  const long long e = ((long long)c + bq - 1) / bq;
-  return t + rt_floor_sum(e + t, r) - rt_floor_sum(e, r);
-}
-__host__ __device__ __forceinline__ long long rt_total(int c, int n_new, int bq) {
-  if (n_new <= 0) return 0;
-  const int nt = (n_new + bq - 1) / bq;
-  return rt_before(c, bq, nt - 1) + rt_tiles(c, n_new, bq, nt - 1) + (long long)RT_UNIT * nt;
-}
-__host__ __device__ __forceinline__ long long rt_begin(long long c, long long W, long long G) { return c * W / G; }
-__host__ __device__ __forceinline__ long long rt_own(long long x, long long W, long long G) { return ((x + 1) * G - 1) / W; }
-
-// A CTA's walk over its range [x, end) of the list. A unit stands there as RT_UNIT
-// + n entries: what it costs before its first tile, then its n key tiles.
-struct RtWalk {
-  long long x, end;
-  int b, zl, t;  // request, (kv head, head group), q tile
-  RaggedSeq s;
-  int c, nt;       // keys before the new tokens, q tiles
-  long long off;   // entries of the unit before x
-  // the current segment: key tiles [j0, j1) of n; key tiles that A and B need
-  // (0 where the unit has no rows for B); the unit's first entry
-  int j0, j1, n, lim[2];
-  long long xs;
-};
-
-__device__ __forceinline__ void rt_load(const RaggedAttnParams& p, int bq, RtWalk& w) {
-  ragged_seq(p, w.b, w.s, false);
-  w.c = max(w.s.kv - w.s.n_new, 0);
-  w.nt = (w.s.n_new + bq - 1) / bq;
-}
-// to entry w.x; pre[i]: entries of one head group of the requests before i * per
-__device__ __forceinline__ void rt_start(const RaggedAttnParams& p, const long long* pre, int HG, int bq, RtWalk& w) {
-  if (w.x >= w.end) return;
-  int lo = 0, hi = RT_PRE - 1;  // the last i whose entries begin at or before x
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] * HG <= w.x) lo = mid; else hi = mid - 1;
-  }
-  long long off = w.x - pre[lo] * HG, per = 0;
-  for (w.b = lo * ((p.B + RT_PRE - 1) / RT_PRE);; ++w.b) {
-    rt_load(p, bq, w);
-    per = rt_total(w.c, w.s.n_new, bq);
-    if (off < per * HG || w.b == p.B - 1) break;
-    off -= per * HG;
-  }
-  w.zl = (int)(off / per);
-  off -= w.zl * per;
-  int a = 0, z = w.nt - 1;
-  while (a < z) {
-    const int mid = (a + z + 1) >> 1;
-    if (rt_before(w.c, bq, mid) + (long long)RT_UNIT * mid <= off) a = mid; else z = mid - 1;
-  }
-  w.t = a;
-  w.off = off - rt_before(w.c, bq, a) - (long long)RT_UNIT * a;
-}
-// the next segment with tiles; false at the end of the range
-__device__ __forceinline__ bool rt_segment(int bq, RtWalk& w) {
-  while (w.x < w.end) {
-    w.n = rt_tiles(w.c, w.s.n_new, bq, w.t);
-    const long long take = min(RT_UNIT + w.n - w.off, w.end - w.x);
-    w.xs = w.x - w.off;
-    w.j0 = (int)max(w.off - RT_UNIT, 0LL);
-    w.j1 = (int)max(w.off + take - RT_UNIT, 0LL);
-    w.x += take;
-    w.off += take;
-    if (w.j1 > w.j0) {
-      const int bh = bq / 2, left = w.s.n_new - w.t * bq;
-      const long long first = (long long)w.c + (long long)w.t * bq + RT_KT - 1;
-      w.lim[0] = (int)((first + min(left, bh)) / RT_KT);
-      w.lim[1] = left > bh ? (int)((first + min(left, bq)) / RT_KT) : 0;
-      return true;
-    }
-  }
-  return false;
-}
-// on to the next unit, where the segment ended its unit
-__device__ __forceinline__ void rt_advance(const RaggedAttnParams& p, int HG, int bq, RtWalk& w) {
-  if (w.x >= w.end) return;
-  w.off = 0;
-  if (++w.t < w.nt) return;
-  w.t = 0;
-  if (++w.zl < HG) return;
-  w.zl = 0;
-  do {
-    ++w.b;
-    rt_load(p, bq, w);
-  } while (w.b < p.B - 1 && w.s.n_new == 0);
-}
 
 // ---- tensor-core and TMEM forms
 
@@ -362,30 +253,8 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  {
-    // prefix sums of the requests' tiles
-    const int per = (p.B + RT_PRE - 1) / RT_PRE;  // the first RT_PRE threads take them
-    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-    long long sum = 0;
-    RaggedSeq s;
-    for (int b = b0; b < b1; ++b) {
-      ragged_seq(p, b, s, blockIdx.x == 0);
-      sum += rt_total(max(s.kv - s.n_new, 0), s.n_new, bq);
-    }
-    long long x = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) s_w[warp] = x;
-    __syncthreads();
-    x -= sum;
-    for (int w = 0; w < warp; ++w) x += s_w[w];
-    if (tid <= RT_PRE) pre[tid] = x;
-  }
   tc_fence_before();
-  __syncthreads();
+  rt_prefix<RT_KT>(p, bq, pre, s_w);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // segment k, or false at the end of the range (or after a timeout); given back by leave()
@@ -551,9 +420,9 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     w.x = cta < G ? rt_begin(cta, W, G) : 0;
     w.end = cta < G ? rt_begin(cta + 1, W, G) : 0;
     const long long xbeg = w.x;
-    rt_start(p, pre, HG, bq, w);
+    rt_start<RT_KT>(p, pre, HG, bq, w);
     for (int k = 0;; ++k) {
-      const bool more = rt_segment(bq, w);
+      const bool more = rt_segment<RT_KT>(bq, w);
       if (!wait_or_abort(&g_empty[k % RT_SEGS], ((k / RT_SEGS) & 1) ^ 1, p.status, abort_flag)) break;
       RtSeg& q = segs[k % RT_SEGS];
       q.j1 = 0;

@@ -46,10 +46,12 @@ int sm_count() {
 
 // Workspace: counters, then partials.
 constexpr size_t WS_COUNTERS = 4096;
-static_assert((RAGGED_TC_CTAS + RAGGED_DECODE_CTAS) * sizeof(int) <= WS_COUNTERS, "counters");
+static_assert((RAGGED_TC_CTAS + RAGGED_DECODE_CTAS) * sizeof(int) <= WS_COUNTERS && RAGGED_F32_CTAS * sizeof(int) <= WS_COUNTERS,
+              "counters");
 
 size_t ws_bytes(int dtype, int D) {
-  return WS_COUNTERS + (dtype == LLAMA_BF16 ? std::max(ragged_tc_ws_floats(D), ragged_decode_ws_floats(D)) * sizeof(float) : 0);
+  return WS_COUNTERS +
+         sizeof(float) * (dtype == LLAMA_BF16 ? std::max(ragged_tc_ws_floats(D), ragged_decode_ws_floats(D)) : ragged_f32_ws_floats(D));
 }
 
 int attn(const RaggedAttnParams& p, int dtype, void* workspace, cudaStream_t st) {
@@ -60,7 +62,7 @@ int attn(const RaggedAttnParams& p, int dtype, void* workspace, cudaStream_t st)
   if (dtype == LLAMA_BF16 && p.tables && p.max_new == 1)
     return launched(launch_attn_ragged_decode(p, part, counters + RAGGED_TC_CTAS, sms, st));
   if (dtype == LLAMA_BF16) return launched(launch_attn_ragged_tc(p, part, counters, sms, st));
-  return launched(launch_attn_ragged_rows<float>(p, st));
+  return launched(launch_attn_ragged_f32(p, part, counters, sms, st));
 }
 
 }  // namespace

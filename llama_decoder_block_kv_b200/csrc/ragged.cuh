@@ -78,6 +78,154 @@ __device__ void ragged_row(const RaggedAttnParams& p, int b, const RaggedSeq& s,
     reinterpret_cast<T*>(p.o)[(row * p.H + h) * D + e * 32 + lane] = from_f32<T>(n > 0 ? o[e] / l : 0.f);
 }
 
+// ---- the list of tiles
+//
+// A unit is a block of query rows of one (request, kv head, group of hpc heads): bq
+// consecutive new tokens x hpc heads; it needs the key tiles (KT keys each) up to its
+// last position. The units, request by request, kv head by kv head, stand in one list
+// that is cut into equal contiguous ranges, one per CTA. A unit takes RT_UNIT entries
+// of it for what it costs besides its tiles, and one per tile.
+constexpr int RT_PRE = 128;  // prefix sums kept, at equal distances over the requests
+constexpr int RT_UNIT = 1;
+
+// q tile t of a request: its key tiles; the sum over the tiles before it (all full)
+template <int KT>
+__host__ __device__ __forceinline__ int rt_tiles(int c, int n_new, int bq, int t) {
+  const long long last = min((long long)(t + 1) * bq, (long long)n_new);
+  return (int)((c + last + KT - 1) / KT);
+}
+__host__ __device__ __forceinline__ long long rt_floor_sum(long long m, int r) {  // sum of i / r over i < m
+  const long long q = m / r;
+  return r * (q * (q - 1) / 2) + q * (m - q * r);
+}
+template <int KT>
+__host__ __device__ __forceinline__ long long rt_before(int c, int bq, long long t) {
+  if (bq >= KT) {
+    const int s = bq / KT;
+    return t * (((long long)c + KT - 1) / KT) + s * (t * (t + 1) / 2);
+  }
+  // ceil((c + (i + 1) bq) / 128) = floor((e + i) / r) + 1 with e = ceil(c / bq), r = 128 / bq
+  const int r = KT / bq;
+  const long long e = ((long long)c + bq - 1) / bq;
+  return t + rt_floor_sum(e + t, r) - rt_floor_sum(e, r);
+}
+template <int KT>
+__host__ __device__ __forceinline__ long long rt_total(int c, int n_new, int bq) {
+  if (n_new <= 0) return 0;
+  const int nt = (n_new + bq - 1) / bq;
+  return rt_before<KT>(c, bq, nt - 1) + rt_tiles<KT>(c, n_new, bq, nt - 1) + (long long)RT_UNIT * nt;
+}
+__host__ __device__ __forceinline__ long long rt_begin(long long c, long long W, long long G) { return c * W / G; }
+__host__ __device__ __forceinline__ long long rt_own(long long x, long long W, long long G) { return ((x + 1) * G - 1) / W; }
+
+// A CTA's walk over its range [x, end) of the list.
+struct RtWalk {
+  long long x, end;
+  int b, zl, t;  // request, (kv head, head group), q tile
+  RaggedSeq s;
+  int c, nt;       // keys before the new tokens, q tiles
+  long long off;   // entries of the unit before x
+  // the current segment: key tiles [j0, j1) of n; key tiles that A and B need
+  // (0 where the unit has no rows for B); the unit's first entry
+  int j0, j1, n, lim[2];
+  long long xs;
+};
+
+__device__ __forceinline__ void rt_load(const RaggedAttnParams& p, int bq, RtWalk& w) {
+  ragged_seq(p, w.b, w.s, false);
+  w.c = max(w.s.kv - w.s.n_new, 0);
+  w.nt = (w.s.n_new + bq - 1) / bq;
+}
+// to entry w.x; pre[i]: entries of one head group of the requests before i * per
+template <int KT>
+__device__ __forceinline__ void rt_start(const RaggedAttnParams& p, const long long* pre, int HG, int bq, RtWalk& w) {
+  if (w.x >= w.end) return;
+  int lo = 0, hi = RT_PRE - 1;  // the last i whose entries begin at or before x
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] * HG <= w.x) lo = mid; else hi = mid - 1;
+  }
+  long long off = w.x - pre[lo] * HG, per = 0;
+  for (w.b = lo * ((p.B + RT_PRE - 1) / RT_PRE);; ++w.b) {
+    rt_load(p, bq, w);
+    per = rt_total<KT>(w.c, w.s.n_new, bq);
+    if (off < per * HG || w.b == p.B - 1) break;
+    off -= per * HG;
+  }
+  w.zl = (int)(off / per);
+  off -= w.zl * per;
+  int a = 0, z = w.nt - 1;
+  while (a < z) {
+    const int mid = (a + z + 1) >> 1;
+    if (rt_before<KT>(w.c, bq, mid) + (long long)RT_UNIT * mid <= off) a = mid; else z = mid - 1;
+  }
+  w.t = a;
+  w.off = off - rt_before<KT>(w.c, bq, a) - (long long)RT_UNIT * a;
+}
+// the next segment with tiles; false at the end of the range
+template <int KT>
+__device__ __forceinline__ bool rt_segment(int bq, RtWalk& w) {
+  while (w.x < w.end) {
+    w.n = rt_tiles<KT>(w.c, w.s.n_new, bq, w.t);
+    const long long take = min(RT_UNIT + w.n - w.off, w.end - w.x);
+    w.xs = w.x - w.off;
+    w.j0 = (int)max(w.off - RT_UNIT, 0LL);
+    w.j1 = (int)max(w.off + take - RT_UNIT, 0LL);
+    w.x += take;
+    w.off += take;
+    if (w.j1 > w.j0) {
+      const int bh = bq / 2, left = w.s.n_new - w.t * bq;
+      const long long first = (long long)w.c + (long long)w.t * bq + KT - 1;
+      w.lim[0] = (int)((first + min(left, bh)) / KT);
+      w.lim[1] = left > bh ? (int)((first + min(left, bq)) / KT) : 0;
+      return true;
+    }
+  }
+  return false;
+}
+// on to the next unit, where the segment ended its unit
+__device__ __forceinline__ void rt_advance(const RaggedAttnParams& p, int HG, int bq, RtWalk& w) {
+  if (w.x >= w.end) return;
+  w.off = 0;
+  if (++w.t < w.nt) return;
+  w.t = 0;
+  if (++w.zl < HG) return;
+  w.zl = 0;
+  do {
+    ++w.b;
+    rt_load(p, bq, w);
+  } while (w.b < p.B - 1 && w.s.n_new == 0);
+}
+
+// Prefix sums of the requests' list entries (one head group), by all threads of a CTA
+// (at least RT_PRE); pre[i]: those of the requests before i * ceil(B / RT_PRE).
+// Ends with a barrier; s_w: a value per warp.
+template <int KT>
+__device__ __forceinline__ void rt_prefix(const RaggedAttnParams& p, int bq, long long* pre, long long* s_w) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per = (p.B + RT_PRE - 1) / RT_PRE;  // the first RT_PRE threads take them
+  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  long long sum = 0;
+  RaggedSeq s;
+  for (int b = b0; b < b1; ++b) {
+    ragged_seq(p, b, s, blockIdx.x == 0);
+    sum += rt_total<KT>(max(s.kv - s.n_new, 0), s.n_new, bq);
+  }
+  long long x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_w[warp] = x;
+  __syncthreads();
+  x -= sum;
+  for (int w = 0; w < warp; ++w) x += s_w[w];
+  if (tid < RT_PRE) pre[tid] = x;
+  if (tid == RT_PRE - 1) pre[RT_PRE] = x + sum;
+  __syncthreads();
+}
+
 // One thread of the warp, as elect.sync names it: the compiler then knows that code under
 // it runs in one thread, and issues tcgen05 instructions without a loop over lanes (8
 // MMAs in 122 cycles against 423 under a test of the lane number, a commit in 5
