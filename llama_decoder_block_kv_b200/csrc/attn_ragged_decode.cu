@@ -493,23 +493,37 @@ __global__ void __launch_bounds__(160, 2)
         const int slot0 = 2 * c0 + (rd_begin(c0, W, G) == P ? 0 : 1);
         for (int e = tid; e < hpc * D / 4; e += 128) {
           const int r = (4 * e) / D, d = 4 * e - r * D;
+          // batches of independent loads: one by one they would cost an L2 round trip each
+          auto slot = [&](int c) { return part + (size_t)(c == c0 ? slot0 : 2 * c) * pstride; };
           float mm = -INFINITY;
-          for (int c = c0; c <= c1; ++c) {
-            const float* pc = part + (size_t)(c == c0 ? slot0 : 2 * c) * pstride;
-            mm = fmaxf(mm, __ldcg(pc + hpc * D + 2 * r));
+          for (int c = c0; c <= c1; c += 16) {
+            float v[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = c + k <= c1 ? __ldcg(slot(c + k) + hpc * D + 2 * r) : -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) mm = fmaxf(mm, v[k]);
           }
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
           float ll = 0.f;
-          for (int c = c0; c <= c1; ++c) {
-            const float* pc = part + (size_t)(c == c0 ? slot0 : 2 * c) * pstride;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pc + hpc * D + 2 * r));
-            const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mm);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(pc + r * D + d));
-            ll += ml.y * f;
-            acc.x += v.x * f;
-            acc.y += v.y * f;
-            acc.z += v.z * f;
-            acc.w += v.w * f;
+          for (int c = c0; c <= c1; c += 8) {
+            float2 ml[8];
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float* pc = slot(min(c + k, c1));
+              ml[k] = __ldcg(reinterpret_cast<const float2*>(pc + hpc * D + 2 * r));
+              v[k] = __ldcg(reinterpret_cast<const float4*>(pc + r * D + d));
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if (c + k > c1) continue;
+              const float f = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - mm);
+              ll += ml[k].y * f;
+              acc.x += v[k].x * f;
+              acc.y += v[k].y * f;
+              acc.z += v[k].z * f;
+              acc.w += v[k].w * f;
+            }
           }
           const float il = 1.f / ll;
           uint2 w;

@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
 
     const bool live = tok0 + 8 * warp / hpc < w.s.n_new;  // a row of this warp is someone's
     int last[4];                                          // last key each row sees
-    float m[4], l[4], o[4][4 * NC];
+    float m[4], l[4];
+    uint64_t o2[4][2 * NC];  // outputs, in pairs of columns
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int tok = tok0 + (4 * ty + i) / hpc;
@@ -113,28 +114,36 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
-      for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.f;
+      for (int c = 0; c < 2 * NC; ++c) o2[i][c] = 0;
     }
     for (int j = w.j0; j < w.j1; ++j) {
       rf_wait_but_one();
       __syncthreads();  // Q, K(j) in; P(j - 1), V(j - 1) read
       float s[4][4];
       if (live) {
+        uint64_t s2[4][4];  // sums over even and over odd d
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        for (int i = 0; i < 4; ++i) s2[i][0] = s2[i][1] = s2[i][2] = s2[i][3] = 0;
 #pragma unroll 4
         for (int d = 0; d < D; d += 4) {
-          float4 q[4], k[4];
+          ulonglong2 q[4], k[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(sQ + (4 * ty + i) * LD + d);
+          for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const ulonglong2*>(sQ + (4 * ty + i) * LD + d);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) k[i] = *reinterpret_cast<const float4*>(sK + (tx + 16 * i) * LD + d);
+          for (int i = 0; i < 4; ++i) k[i] = *reinterpret_cast<const ulonglong2*>(sK + (tx + 16 * i) * LD + d);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              s[i][c] = fmaf(q[i].x, k[c].x, fmaf(q[i].y, k[c].y, fmaf(q[i].z, k[c].z, fmaf(q[i].w, k[c].w, s[i][c]))));
+            for (int c = 0; c < 4; ++c) s2[i][c] = rt_fma2(q[i].x, k[c].x, rt_fma2(q[i].y, k[c].y, s2[i][c]));
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float even, odd;
+            rt_split(s2[i][c], even, odd);
+            s[i][c] = even + odd;
+          }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float mt = -INFINITY;
@@ -156,7 +165,7 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
           }
           l[i] = l[i] * a + sum;  // of this thread's keys
 #pragma unroll
-          for (int c = 0; c < 4 * NC; ++c) o[i][c] *= a;
+          for (int c = 0; c < 2 * NC; ++c) o2[i][c] = rt_mul2(o2[i][c], rt_f2(a, a));
         }
       }
       __syncthreads();  // K(j) read
@@ -176,14 +185,12 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
           for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-              const float4 v = *reinterpret_cast<const float4*>(sV + (k + kk) * D + 64 * c + 4 * tx);
+              const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sV + (k + kk) * D + 64 * c + 4 * tx);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const float e = kk == 0 ? pr[i].x : kk == 1 ? pr[i].y : kk == 2 ? pr[i].z : pr[i].w;
-                o[i][4 * c] = fmaf(e, v.x, o[i][4 * c]);
-                o[i][4 * c + 1] = fmaf(e, v.y, o[i][4 * c + 1]);
-                o[i][4 * c + 2] = fmaf(e, v.z, o[i][4 * c + 2]);
-                o[i][4 * c + 3] = fmaf(e, v.w, o[i][4 * c + 3]);
+                o2[i][2 * c] = rt_fma2(rt_f2(e, e), v.x, o2[i][2 * c]);
+                o2[i][2 * c + 1] = rt_fma2(rt_f2(e, e), v.y, o2[i][2 * c + 1]);
               }
             }
         }
@@ -199,6 +206,11 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
 #pragma unroll
       for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
 
+    float o[4][4 * NC];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < 2 * NC; ++c) rt_split(o2[i][c], o[i][2 * c], o[i][2 * c + 1]);
     bool bad[4] = {false, false, false, false};  // the row's result is not finite
     // normalise and store row i of this thread (columns 4 tx + 64 c)
     auto finish = [&](int i, float sum) {
@@ -237,32 +249,61 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
       __syncthreads();
       if (s_last) {
         const int slot0 = 2 * c0 + (w.xs <= rt_begin(c0, W, G) ? 0 : 1);
+// batches of independent loads: one by one they would cost an L2 round trip each
+        auto slot = [&](int c) { return part + (size_t)(c == c0 ? slot0 : 2 * c) * stride; };
+        float mm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, ll[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int c = c0; c <= c1; c += 8) {
+          float v[8][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 4 * ty + i;
-          if (tok0 + r / hpc >= w.s.n_new) continue;
-          float mm = -INFINITY, ll = 0.f;
-          for (int c = c0; c <= c1; ++c)
-            mm = fmaxf(mm, __ldcg(reinterpret_cast<const float2*>(part + (size_t)(c == c0 ? slot0 : 2 * c) * stride + RF_ROWS * D) + r).x);
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              v[k][i] = c + k <= c1 && tok0 + (4 * ty + i) / hpc < w.s.n_new
+                            ? __ldcg(reinterpret_cast<const float2*>(slot(c + k) + RF_ROWS * D) + 4 * ty + i).x
+                            : -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mm[i] = fmaxf(mm[i], v[k][i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int c = 0; c < 4 * NC; ++c) o[i][c] = 0.f;
-          for (int c = c0; c <= c1; ++c) {
-            const float* pc = part + (size_t)(c == c0 ? slot0 : 2 * c) * stride;
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(pc + RF_ROWS * D) + r);
-            if (ml.x == -INFINITY) continue;
-            const float f = exp2f(ml.x - mm);
-            ll += ml.y * f;
+        for (int c = c0; c <= c1; c += 2) {
+          float2 ml[2][4];
+          float4 v[2][4][NC];
 #pragma unroll
-            for (int k = 0; k < NC; ++k) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(pc + r * D + 64 * k + 4 * tx));
-              o[i][4 * k] += v.x * f;
-              o[i][4 * k + 1] += v.y * f;
-              o[i][4 * k + 2] += v.z * f;
-              o[i][4 * k + 3] += v.w * f;
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 4 * ty + i;
+              const bool have = c + k <= c1 && tok0 + r / hpc < w.s.n_new;
+              const float* pc = slot(have ? c + k : c0);
+              ml[k][i] = have ? __ldcg(reinterpret_cast<const float2*>(pc + RF_ROWS * D) + r) : make_float2(-INFINITY, 0.f);
+#pragma unroll
+              for (int e = 0; e < NC; ++e)
+                v[k][i][e] = have ? __ldcg(reinterpret_cast<const float4*>(pc + r * D + 64 * e + 4 * tx))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-          }
-          finish(i, ll);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (ml[k][i].x == -INFINITY) continue;  // no weight there
+              const float f = exp2f(ml[k][i].x - mm[i]);
+              ll[i] += ml[k][i].y * f;
+#pragma unroll
+              for (int e = 0; e < NC; ++e) {
+                o[i][4 * e] += v[k][i][e].x * f;
+                o[i][4 * e + 1] += v[k][i][e].y * f;
+                o[i][4 * e + 2] += v[k][i][e].z * f;
+                o[i][4 * e + 3] += v[k][i][e].w * f;
+              }
+            }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) finish(i, ll[i]);
         if (tid == 0) counters[c0] = 0;  // re-armed for the next launch
       }
       __syncthreads();  // s_last is written again by the next cut segment

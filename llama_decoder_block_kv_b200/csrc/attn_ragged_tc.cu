@@ -155,24 +155,6 @@ __device__ __forceinline__ void rt_st16(uint32_t taddr, const uint32_t* r) {
 }
 __device__ __forceinline__ void rt_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ uint64_t rt_f2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void rt_split(uint64_t r, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
-}
-__device__ __forceinline__ uint64_t rt_fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t rt_add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ float rt_max3(float a, float b, float c) {  // NaN where one is
   float d;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -685,41 +667,61 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
           // unless its range starts inside it, the others in their first
           const int slot0 = w.slot0;
           if (store) {
-            float mm = -INFINITY;
-            for (int c = c0; c <= c1; ++c)
-              mm = fmaxf(mm, __ldcg(reinterpret_cast<const float2*>(part + (size_t)(c == c0 ? slot0 : 2 * c) * stride + 256 * D) + row).x);
-            float ll = 0.f;
-            for (int c = c0; c <= c1; ++c) {
-              const float2 ml = __ldcg(reinterpret_cast<const float2*>(part + (size_t)(c == c0 ? slot0 : 2 * c) * stride + 256 * D) + row);
-              if (ml.x != -INFINITY) ll += ml.y * rt_ex2(ml.x - mm);
+            // batches of independent loads: one by one they would cost an L2 round trip each
+            auto slot = [&](int c) { return part + (size_t)(c == c0 ? slot0 : 2 * c) * stride; };
+            float mm = -INFINITY, ll = 0.f;
+            for (int c = c0; c <= c1; c += 16) {
+              float2 v[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                v[k] = c + k <= c1 ? __ldcg(reinterpret_cast<const float2*>(slot(c + k) + 256 * D) + row)
+                                   : make_float2(-INFINITY, 0.f);
+              float mn = mm;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) mn = fmaxf(mn, v[k].x);
+              if (mm != -INFINITY) ll *= rt_ex2(mm - mn);
+              mm = mn;
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if (v[k].x != -INFINITY) ll += v[k].y * rt_ex2(v[k].x - mm);
             }
             const float inv = last < 0 ? 0.f : 1.f / ll;
 #pragma unroll 1
-            for (int d = 0; d < D; d += 16) {
-              float acc[16];
+            for (int d = 0; d < D; d += 32) {
+              float acc[32];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-              for (int c = c0; c <= c1; ++c) {
-                const float* pc = part + (size_t)(c == c0 ? slot0 : 2 * c) * stride;
-                const float m_c = __ldcg(reinterpret_cast<const float2*>(pc + 256 * D) + row).x;
-                if (m_c == -INFINITY) continue;  // no weight there (and perhaps no O)
-                const float f = rt_ex2(m_c - mm);
+              for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+#pragma unroll 1
+              for (int c = c0; c <= c1; c += 2) {
+                float m_c[2];
+                float4 v[2][8];
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                  const float4 v = __ldcg(reinterpret_cast<const float4*>(pc) + ((d + e) / 4) * 256 + row);
-                  acc[e] += v.x * f;
-                  acc[e + 1] += v.y * f;
-                  acc[e + 2] += v.z * f;
-                  acc[e + 3] += v.w * f;
+                for (int k = 0; k < 2; ++k) {
+                  const float* pc = slot(min(c + k, c1));
+                  m_c[k] = c + k <= c1 ? __ldcg(reinterpret_cast<const float2*>(pc + 256 * D) + row).x : -INFINITY;
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) v[k][e] = __ldcg(reinterpret_cast<const float4*>(pc) + (d / 4 + e) * 256 + row);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  if (m_c[k] == -INFINITY) continue;  // no weight there (and perhaps no O)
+                  const float f = rt_ex2(m_c[k] - mm);
+#pragma unroll
+                  for (int e = 0; e < 8; ++e) {
+                    acc[4 * e] += v[k][e].x * f;
+                    acc[4 * e + 1] += v[k][e].y * f;
+                    acc[4 * e + 2] += v[k][e].z * f;
+                    acc[4 * e + 3] += v[k][e].w * f;
+                  }
                 }
               }
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
+              for (int e = 0; e < 32; ++e) {
                 acc[e] = last < 0 ? 0.f : acc[e] * inv;
                 bad |= !(fabsf(acc[e]) < INFINITY);
               }
-              store8(dst + d, acc);
-              store8(dst + d + 8, acc + 8);
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) store8(dst + d + e, acc + e);
             }
           }
           if (tid == RT_LEADER) counters[c0] = 0;  // re-armed for the next launch

@@ -226,6 +226,30 @@ __device__ __forceinline__ void rt_prefix(const RaggedAttnParams& p, int bq, lon
   __syncthreads();
 }
 
+// packed fp32 arithmetic: two lanes of a 64-bit register per instruction
+__device__ __forceinline__ uint64_t rt_f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void rt_split(uint64_t r, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t rt_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t rt_mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t rt_add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 // One thread of the warp, as elect.sync names it: the compiler then knows that code under
 // it runs in one thread, and issues tcgen05 instructions without a loop over lanes (8
 // MMAs in 122 cycles against 423 under a test of the lane number, a commit in 5
