@@ -591,6 +591,26 @@ int llama_attn_packed(int dtype, int n_heads, int n_kv_heads, int head_dim, cons
                       void* workspace_dev, int64_t workspace_bytes, int32_t* status_dev, void* cuda_stream);
 
 /*
+ * llama_block_forward over a paged cache: one TransformerBlock.forward in place on the
+ * fp32 residual stream h_dev [n_tokens][dim] of packed tokens. The rows of q, k and v are
+ * rotated and appended as by llama_rope_append (positions below the context's max_seq_len),
+ * the attention is llama_attn_paged, with the arguments of both; the pages hold K in the
+ * interleaved pairs of the notes whatever the context's rope_half_split. args has the
+ * context's heads, head_dim and dtype. Rows of tokens with slot -1 are unspecified
+ * afterwards. workspace_dev: llama_block_paged_workspace_bytes(ctx, n_tokens) bytes, zeroed
+ * once, under the rules of llama_attn_workspace_bytes; one workspace serves all layers of a
+ * step. Runs on the context's device; the first call of more tokens than reserved
+ * (llama_reserve) allocates, so reserve before a capture. Like the context's other calls,
+ * not to be overlapped with another call of the same context.
+ */
+int64_t llama_block_paged_workspace_bytes(llama_ctx* ctx, int n_tokens);
+int llama_block_forward_paged(llama_ctx* ctx, int layer, float* h_dev, const llama_page_args* args,
+                              void* k_pages_dev, void* v_pages_dev, const int32_t* block_tables_dev,
+                              const int32_t* cu_dev, const int32_t* kv_lens_dev, const int32_t* positions_dev,
+                              const int32_t* slots_dev, int n_seqs, int n_tokens, int max_new, void* workspace_dev,
+                              int64_t workspace_bytes, int32_t* status_dev, void* cuda_stream);
+
+/*
  * Synchronise the device, return and clear *status_dev: LLAMA_OK or the most
  * severe of LLAMA_ERR_TIMEOUT, LLAMA_ERR_PAGE_RANGE, LLAMA_ERR_OUT_OF_PAGES,
  * LLAMA_ERR_POS_RANGE; *flags (if not NULL) receives the raw bits.

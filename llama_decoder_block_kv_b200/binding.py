@@ -45,7 +45,8 @@ EXPORTED = ("llama_ffn_hidden", "llama_create", "llama_destroy", "llama_set_laye
             "llama_set_decode_attention", "llama_set_decode_linear_mma", "llama_tile_weights",
             "llama_selftest_bounded_wait", "llama_set_alloc_limit", "llama_allocated_bytes",
             "llama_selfcheck_plans", "llama_page_plan", "llama_rope_append", "llama_attn_workspace_bytes",
-            "llama_attn_paged", "llama_attn_packed", "llama_paged_status")
+            "llama_attn_paged", "llama_attn_packed", "llama_paged_status", "llama_block_paged_workspace_bytes",
+            "llama_block_forward_paged")
 
 
 class LlamaArgs(ctypes.Structure):
@@ -115,12 +116,15 @@ def lib() -> ctypes.CDLL:
         L.llama_attn_workspace_bytes.argtypes = [i] * 4
         L.llama_attn_paged.argtypes = [pa, vp, i64] + [vp] * 5 + [i, i, i, vp, vp, i64, vp, vp]
         L.llama_attn_packed.argtypes = [i] * 4 + [vp, i64] * 3 + [vp, i, i, i, vp, vp, i64, vp, vp]
+        L.llama_block_paged_workspace_bytes.argtypes = [vp, i]
+        L.llama_block_forward_paged.argtypes = [vp, i, vp, pa] + [vp] * 7 + [i, i, i, vp, i64, vp, vp]
         L.llama_paged_status.argtypes = [vp, ctypes.POINTER(i)]
         for name in EXPORTED:
             if name not in ("llama_destroy", "llama_strerror"):
                 getattr(L, name).restype = ctypes.c_int
         L.llama_allocated_bytes.restype = ctypes.c_uint64
         L.llama_attn_workspace_bytes.restype = ctypes.c_int64
+        L.llama_block_paged_workspace_bytes.restype = ctypes.c_int64
         _lib = L
     return _lib
 
@@ -485,6 +489,31 @@ def llama_attn_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: tor
         _CODE[dt], H, Hkv, D, qp, qs, kp, ks, vp, vs, _whole("cu", cu, i32, (-1,), d), cu.shape[0] - 1, n, int(max_len),
         _whole("out", out, dt, (n, H, D), d), _whole("workspace", workspace, torch.uint8, (-1,), d), workspace.shape[0],
         _whole("status", status, i32, (1,), d), _raw_stream(stream)), "llama_attn_packed")
+
+
+def llama_block_paged_workspace_bytes(ctx, n_tokens: int) -> int:
+    """Bytes of the (zeroed, uint8) workspace of llama_block_forward_paged."""
+    n = lib().llama_block_paged_workspace_bytes(ctx, n_tokens)
+    if n < 0:
+        raise LlamaError(n, "llama_block_paged_workspace_bytes")
+    return n
+
+
+def llama_block_forward_paged(ctx, layer: int, h: torch.Tensor, args: PageArgs, k_pages: torch.Tensor,
+                              v_pages: torch.Tensor, block_tables: torch.Tensor, cu: torch.Tensor, kv_lens: torch.Tensor,
+                              positions: torch.Tensor, slots: torch.Tensor, max_new: int, workspace: torch.Tensor,
+                              status: torch.Tensor, stream=None) -> None:
+    """h fp32 [n][dim] in place; the other tensors as in llama_rope_append and llama_attn_paged, on one device."""
+    d, i32, dt = torch.cuda.current_device(), torch.int32, _TORCH[args.dtype]
+    n, B = h.shape[0], kv_lens.shape[0]
+    pool = (args.num_pages, args.n_kv_heads, args.page_size, args.head_dim)
+    _check(lib().llama_block_forward_paged(
+        ctx, layer, _whole("h", h, torch.float32, (n, args.n_heads * args.head_dim), d), args.ref(), _whole("k_pages", k_pages, dt, pool, d),
+        _whole("v_pages", v_pages, dt, pool, d), _whole("block_tables", block_tables, i32, (B, args.max_pages), d),
+        _whole("cu", cu, i32, (B + 1,), d), _whole("kv_lens", kv_lens, i32, (B,), d),
+        _whole("positions", positions, i32, (n,), d), _whole("slots", slots, i32, (n,), d), B, n, int(max_new),
+        _whole("workspace", workspace, torch.uint8, (-1,), d), workspace.shape[0], _whole("status", status, i32, (1,), d),
+        _raw_stream(stream)), "llama_block_forward_paged")
 
 
 def llama_paged_status(status: torch.Tensor):

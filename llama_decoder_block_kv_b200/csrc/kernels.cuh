@@ -218,6 +218,13 @@ struct RaggedAttnParams {
   int* status;
 };
 
+// paged_api.cu: the checks of the header's page arguments, and the kernel that suits a
+// call (LLAMA_ code; workspace: ragged_ws_bytes, zeroed once)
+int page_shift(int page_size);  // -1: not a page size
+bool page_args_ok(const llama_page_args* a);
+size_t ragged_ws_bytes(int dtype, int D);
+int ragged_attention(const RaggedAttnParams& p, int dtype, void* workspace, cudaStream_t st);
+
 // attn_ragged_f32.cu: partials and counters of RAGGED_F32_CTAS CTAs
 constexpr int RAGGED_F32_CTAS = 592;  // at most this many CTAs: four per SM (head_dim 64), or two
 size_t ragged_f32_ws_floats(int D);

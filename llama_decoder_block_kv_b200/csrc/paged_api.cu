@@ -10,8 +10,6 @@ namespace {
 
 bool aligned(const void* p, size_t a = 16) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-int page_shift(int ps) { return ps == 16 ? 4 : ps == 32 ? 5 : ps == 64 ? 6 : ps == 128 ? 7 : -1; }
-
 bool heads_ok(int dtype, int H, int Hkv, int D) {
   return (dtype == LLAMA_FP32 || dtype == LLAMA_BF16) && H >= 1 && Hkv >= 1 && H % Hkv == 0 && H <= (1 << 16) &&
          (D == 64 || D == 128);
@@ -20,11 +18,6 @@ bool heads_ok(int dtype, int H, int Hkv, int D) {
 bool pool_ok(const llama_page_args* a) {
   return a && page_shift(a->page_size) > 0 && a->num_pages >= 1 && a->max_pages >= 1 &&
          (long long)a->max_pages * a->page_size < (1LL << 31) && (long long)a->num_pages * a->page_size < (1LL << 31);
-}
-
-bool args_ok(const llama_page_args* a) {
-  return pool_ok(a) && heads_ok(a->dtype, a->n_heads, a->n_kv_heads, a->head_dim) &&
-         (long long)a->num_pages * a->n_kv_heads * a->page_size < (1LL << 31);
 }
 
 bool stride_ok(int64_t stride, int64_t width, int esz) {
@@ -44,17 +37,28 @@ int sm_count() {
   return n;
 }
 
+}  // namespace
+
+namespace llama {
+
+int page_shift(int ps) { return ps == 16 ? 4 : ps == 32 ? 5 : ps == 64 ? 6 : ps == 128 ? 7 : -1; }
+
+bool page_args_ok(const llama_page_args* a) {
+  return pool_ok(a) && heads_ok(a->dtype, a->n_heads, a->n_kv_heads, a->head_dim) &&
+         (long long)a->num_pages * a->n_kv_heads * a->page_size < (1LL << 31);
+}
+
 // Workspace: counters, then partials.
-constexpr size_t WS_COUNTERS = 4096;
+static constexpr size_t WS_COUNTERS = 4096;
 static_assert((RAGGED_TC_CTAS + RAGGED_DECODE_CTAS) * sizeof(int) <= WS_COUNTERS && RAGGED_F32_CTAS * sizeof(int) <= WS_COUNTERS,
               "counters");
 
-size_t ws_bytes(int dtype, int D) {
+size_t ragged_ws_bytes(int dtype, int D) {
   return WS_COUNTERS +
          sizeof(float) * (dtype == LLAMA_BF16 ? std::max(ragged_tc_ws_floats(D), ragged_decode_ws_floats(D)) : ragged_f32_ws_floats(D));
 }
 
-int attn(const RaggedAttnParams& p, int dtype, void* workspace, cudaStream_t st) {
+int ragged_attention(const RaggedAttnParams& p, int dtype, void* workspace, cudaStream_t st) {
   const int sms = sm_count();
   if (sms <= 0) return LLAMA_ERR_CUDA;
   int* counters = static_cast<int*>(workspace);
@@ -65,7 +69,7 @@ int attn(const RaggedAttnParams& p, int dtype, void* workspace, cudaStream_t st)
   return launched(launch_attn_ragged_f32(p, part, counters, sms, st));
 }
 
-}  // namespace
+}  // namespace llama
 
 extern "C" {
 
@@ -100,7 +104,7 @@ int llama_page_plan(const llama_page_args* a, const int32_t* cached, const int32
 int llama_rope_append(const llama_page_args* a, const void* qkv, int64_t qkv_stride, int qkv_dtype,
                       const int32_t* positions, const int32_t* slots, int n_tokens, const float* rope, int n_pos,
                       void* q_out, void* k_pages, void* v_pages, int32_t* status, void* stream) {
-  if (!args_ok(a) || n_tokens < 1 || n_pos < 1) return LLAMA_ERR_INVALID_ARGS;
+  if (!page_args_ok(a) || n_tokens < 1 || n_pos < 1) return LLAMA_ERR_INVALID_ARGS;
   if (qkv_dtype != LLAMA_FP32 && (qkv_dtype != LLAMA_BF16 || a->dtype != LLAMA_BF16)) return LLAMA_ERR_INVALID_ARGS;
   const int64_t width = (int64_t)(a->n_heads + 2 * a->n_kv_heads) * a->head_dim;
   if (!stride_ok(qkv_stride, width, qkv_dtype == LLAMA_BF16 ? 2 : 4)) return LLAMA_ERR_INVALID_ARGS;
@@ -130,14 +134,14 @@ int llama_rope_append(const llama_page_args* a, const void* qkv, int64_t qkv_str
 
 int64_t llama_attn_workspace_bytes(int dtype, int n_heads, int n_kv_heads, int head_dim) {
   if (!heads_ok(dtype, n_heads, n_kv_heads, head_dim)) return LLAMA_ERR_INVALID_ARGS;
-  return (int64_t)ws_bytes(dtype, head_dim);
+  return (int64_t)ragged_ws_bytes(dtype, head_dim);
 }
 
 int llama_attn_paged(const llama_page_args* a, const void* q, int64_t q_stride, const void* k_pages,
                      const void* v_pages, const int32_t* tables, const int32_t* cu, const int32_t* kv_lens, int n_seqs,
                      int n_tokens, int max_new, void* out, void* workspace, int64_t workspace_bytes, int32_t* status,
                      void* stream) {
-  if (!args_ok(a) || n_seqs < 1 || n_seqs > LLAMA_MAX_SEQS || n_tokens < 1 || max_new < 1)
+  if (!page_args_ok(a) || n_seqs < 1 || n_seqs > LLAMA_MAX_SEQS || n_tokens < 1 || max_new < 1)
     return LLAMA_ERR_INVALID_ARGS;
   if (!stride_ok(q_stride, (int64_t)a->n_heads * a->head_dim, a->dtype == LLAMA_BF16 ? 2 : 4))
     return LLAMA_ERR_INVALID_ARGS;
@@ -164,7 +168,7 @@ int llama_attn_paged(const llama_page_args* a, const void* q, int64_t q_stride, 
   p.max_pages = a->max_pages;
   p.o = out;
   p.status = status;
-  return attn(p, a->dtype, workspace, reinterpret_cast<cudaStream_t>(stream));
+  return ragged_attention(p, a->dtype, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int llama_attn_packed(int dtype, int n_heads, int n_kv_heads, int head_dim, const void* q, int64_t q_stride,
@@ -198,7 +202,7 @@ int llama_attn_packed(int dtype, int n_heads, int n_kv_heads, int head_dim, cons
   p.D = head_dim;
   p.o = out;
   p.status = status;
-  return attn(p, dtype, workspace, reinterpret_cast<cudaStream_t>(stream));
+  return ragged_attention(p, dtype, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int llama_paged_status(int32_t* status, int* flags) {

@@ -311,12 +311,22 @@ bool use_stream_k(int mode, const DecodeSkPlan& sk, int max_len, int num_sms) {
   return sk.hpc <= 8 && w_max >= 8LL * num_sms;
 }
 
-int run_block(llama_ctx* c, int layer, float* h, int B, int T, const int* sp_dev, int sp_host, cudaStream_t st) {
+// A paged call's tokens and cache: the QKV sums go to `qkv` in fp32, from there to q and
+// the pages, and the attention runs over the pages.
+struct PagedCall {
+  float* qkv;
+  RopeAppendParams append;
+  RaggedAttnParams attn;
+  void* attn_ws;
+};
+
+int run_block(llama_ctx* c, int layer, float* h, int B, int T, const int* sp_dev, int sp_host, cudaStream_t st,
+              const PagedCall* paged = nullptr) {
   Layer& Ly = c->layers[layer];
   const int M = B * T;
   const int HD = c->H * c->D;
   int r;
-  if (T == 1 && c->decode_mode == LLAMA_DECODE_PERSISTENT) {
+  if (!paged && T == 1 && c->decode_mode == LLAMA_DECODE_PERSISTENT) {
     if (!c->bf16 || !c->gbar) return LLAMA_ERR_INVALID_ARGS;
     r = run_block_persistent(c, layer, h, B, sp_dev, sp_host, st);
     return r == 1 ? LLAMA_ERR_INVALID_ARGS : r;
@@ -327,7 +337,11 @@ int run_block(llama_ctx* c, int layer, float* h, int B, int T, const int* sp_dev
                     cudaSuccess)
     return LLAMA_ERR_CUDA;
 
-  EpiParams e = epi_base(c, EPI_QKV_ROPE, M, c->n_qkv);
+  EpiParams e = epi_base(c, paged ? EPI_STORE_F32 : EPI_QKV_ROPE, M, c->n_qkv);
+  if (paged) {
+    e.out = paged->qkv;
+    e.ld_out = c->n_qkv;
+  }
   e.q_out = c->q;
   e.cache_k = Ly.cache_k;
   e.cache_v = Ly.cache_v;
@@ -344,7 +358,11 @@ int run_block(llama_ctx* c, int layer, float* h, int B, int T, const int* sp_dev
     return r;
 
   cudaError_t ce;
-  if (!c->bf16) {
+  if (paged) {
+    if (launch_rope_append(paged->append, false, c->bf16, st) != cudaSuccess) return LLAMA_ERR_CUDA;
+    if ((r = ragged_attention(paged->attn, c->bf16 ? LLAMA_BF16 : LLAMA_FP32, paged->attn_ws, st))) return r;
+    ce = cudaSuccess;
+  } else if (!c->bf16) {
     ce = launch_attn_simple<float>(c->q, Ly.cache_k, Ly.cache_v, c->o, sp_dev, sp_host, B, T, c->H, c->Hkv, c->D,
                                    c->S, st);
   } else if (T == 1) {
@@ -728,6 +746,70 @@ int llama_block_forward(llama_ctx* c, int layer, float* h, int B, int T, const i
   if (!start_pos_dev && (host_start_pos < 0 || (long)host_start_pos + T > c->S)) return LLAMA_ERR_INVALID_ARGS;
   if ((r = reserve(c, B * T))) return r;
   return run_block(c, layer, h, B, T, start_pos_dev, host_start_pos, S_(stream));
+}
+
+int64_t llama_block_paged_workspace_bytes(llama_ctx* c, int n_tokens) {
+  if (!c || n_tokens < 1) return LLAMA_ERR_INVALID_ARGS;
+  return (int64_t)(round256(ragged_ws_bytes(c->bf16 ? LLAMA_BF16 : LLAMA_FP32, c->D)) + (size_t)n_tokens * c->n_qkv * 4);
+}
+
+int llama_block_forward_paged(llama_ctx* c, int layer, float* h, const llama_page_args* a, void* k_pages, void* v_pages,
+                              const int32_t* tables, const int32_t* cu, const int32_t* kv_lens, const int32_t* positions,
+                              const int32_t* slots, int n_seqs, int n_tokens, int max_new, void* workspace,
+                              int64_t workspace_bytes, int32_t* status, void* stream) {
+  auto aligned = [](const void* p, size_t n) { return p && reinterpret_cast<uintptr_t>(p) % n == 0; };
+  if (!c || layer < 0 || layer >= c->L || !page_args_ok(a)) return LLAMA_ERR_INVALID_ARGS;
+  if (a->dtype != (c->bf16 ? LLAMA_BF16 : LLAMA_FP32) || a->n_heads != c->H || a->n_kv_heads != c->Hkv || a->head_dim != c->D)
+    return LLAMA_ERR_INVALID_ARGS;
+  if (n_seqs < 1 || n_seqs > LLAMA_MAX_SEQS || n_tokens < 1 || max_new < 1) return LLAMA_ERR_INVALID_ARGS;
+  if (!aligned(h, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(tables, 4) || !aligned(cu, 4) ||
+      !aligned(kv_lens, 4) || !aligned(positions, 4) || !aligned(slots, 4) || !aligned(workspace, 256) ||
+      !aligned(status, 4) || workspace_bytes < llama_block_paged_workspace_bytes(c, n_tokens))
+    return LLAMA_ERR_INVALID_ARGS;
+  if (!c->layers[layer].set) return LLAMA_ERR_NOT_READY;
+  if (cudaSetDevice(c->device) != cudaSuccess) return LLAMA_ERR_CUDA;
+  int r;
+  if ((r = reserve(c, n_tokens))) return r;
+  PagedCall pc = {};
+  pc.attn_ws = workspace;
+  pc.qkv = reinterpret_cast<float*>(static_cast<char*>(workspace) + round256(ragged_ws_bytes(a->dtype, c->D)));
+  RopeAppendParams& p = pc.append;
+  p.qkv = pc.qkv;
+  p.stride = c->n_qkv;
+  p.positions = positions;
+  p.slots = slots;
+  p.N = n_tokens;
+  p.H = c->H;
+  p.Hkv = c->Hkv;
+  p.D = c->D;
+  p.page_shift = page_shift(a->page_size);
+  p.num_pages = a->num_pages;
+  p.n_pos = c->S;
+  p.rope = c->rope;
+  p.q_out = c->q;
+  p.k_pages = k_pages;
+  p.v_pages = v_pages;
+  p.status = status;
+  RaggedAttnParams& t = pc.attn;
+  t.q = c->q;
+  t.q_stride = (long long)c->H * c->D;
+  t.k = k_pages;
+  t.v = v_pages;
+  t.tables = tables;
+  t.cu = cu;
+  t.kv_lens = kv_lens;
+  t.B = n_seqs;
+  t.N = n_tokens;
+  t.max_new = std::min(max_new, n_tokens);
+  t.H = c->H;
+  t.Hkv = c->Hkv;
+  t.D = c->D;
+  t.page_shift = p.page_shift;
+  t.num_pages = a->num_pages;
+  t.max_pages = a->max_pages;
+  t.o = c->o;
+  t.status = status;
+  return run_block(c, layer, h, 1, n_tokens, nullptr, 0, S_(stream), &pc);
 }
 
 int llama_generate(llama_ctx* c, int32_t* tokens, const uint8_t* prompt_mask, int B, int total_len,

@@ -557,3 +557,114 @@ def test_binding_refuses_what_the_calls_cannot_take():
         call(ws=p.ws[:-1])
     with pytest.raises(ValueError):
         B.PageArgs(4, 2, 64, 16, 8, 2, "fp16")
+
+
+# ------------------------------------------------------------------ a block over a paged cache
+
+@pytest.mark.parametrize("act,dim,H,Hkv,page", [("fp32", 256, 4, 2, 16), ("bf16", 512, 4, 2, 32), ("bf16", 1024, 8, 8, 16),
+                                                ("bf16", 2048, 32, 4, 128)])
+def test_block_over_a_paged_cache(act, dim, H, Hkv, page):
+    """Requests of different lengths through one block: prompts, a chunk beside single tokens, then single tokens from
+    a captured step (plan and block) that is replayed; each request against an oracle block with a cache of its own."""
+    import oracle as O
+    from llama_decoder_block_kv_b200 import synth
+    from tests.gpu_util import BF16_HIDDEN_ABS, Pair, assert_abs_close, assert_fp32_close
+    from tests.helpers import build_oracle, t2np
+
+    D = dim // H
+    w = synth.Workload(name=f"paged block dim {dim} H {H}/{Hkv}", dim=dim, n_layers=1, n_heads=H, n_kv_heads=Hkv,
+                       ffn_hidden=O.ffn_hidden_dim(dim, 256), vocab_size=0, multiple_of=256, ffn_dim_multiplier=None, norm_eps=1e-5,
+                       rope_theta=10000.0, max_batch_size=2, max_seq_len=256, act=act, batch=2, seed=9, norm_weights="random")
+    pair = Pair(w)
+    try:
+        lw = [{k: v.cpu() for k, v in synth.layer_weights(w, 0, device="cpu").items()}]
+        n_req, P, cols, T = 3, 3 * (256 // page), 256 // page, 130
+        oracles = [build_oracle(w, lw, None) for _ in range(n_req)]
+        a = B.PageArgs(H, Hkv, D, page, P, cols, act)
+        kp, vp = (torch.full((P, Hkv, page, D), float("nan"), dtype=DT[act], device="cuda") for _ in range(2))
+        table = torch.full((n_req, cols), -1, dtype=torch.int32, device="cuda")
+        free, count = torch.arange(P, dtype=torch.int32, device="cuda"), ints([P])
+        kv, cu = torch.zeros(n_req, dtype=torch.int32, device="cuda"), torch.zeros(n_req + 1, dtype=torch.int32, device="cuda")
+        st = status_word()
+        ws = torch.zeros(B.llama_block_paged_workspace_bytes(pair.ctx, T), dtype=torch.uint8, device="cuda")
+
+        def step(new, h, pos, slot, max_new):
+            B.llama_page_plan(a, kv, new, table, free, count, count, cu, kv, pos, slot, st)
+            B.llama_block_forward_paged(pair.ctx, 0, h, a, kp, vp, table, cu, kv, pos, slot, max_new, ws, st)
+
+        def check(h, rows, have, new, what):
+            assert B.llama_paged_status(st) == (B.LLAMA_OK, 0)
+            pair.check_error()
+            t = 0
+            for b, n in enumerate(new):
+                if n:
+                    ref = oracles[b].block(0, t2np(rows[t:t + n])[None], have[b])[0]
+                    got = t2np(h[t:t + n])
+                    if act == "fp32":
+                        assert_fp32_close(got, ref, (what, b))
+                    else:
+                        assert_abs_close(got, ref, BF16_HIDDEN_ABS, (what, b))
+                t += n
+
+        have = [0] * n_req
+        for i, new in enumerate(([77, 33, 0], [40, 1, 12], [1, 1, 100], [1, 5, 1])):
+            n = sum(new)
+            rows = synth.hidden(w, (1, n, dim), call=i)[0]
+            h = rows.to("cuda").contiguous()
+            pos, slot = (torch.zeros(n, dtype=torch.int32, device="cuda") for _ in range(2))
+            step(ints(new), h, pos, slot, max(new))
+            check(h, rows, have, new, i)
+            have = [x + y for x, y in zip(have, new)]
+        rows = synth.hidden(w, (1, 4 * n_req, dim), call=9)[0]
+        h, one = torch.zeros((n_req, dim), device="cuda"), ints([1] * n_req)
+        pos, slot = (torch.zeros(n_req, dtype=torch.int32, device="cuda") for _ in range(2))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(one, h, pos, slot, 1)
+        for i in range(4):
+            h.copy_(rows[i * n_req:(i + 1) * n_req])
+            g.replay()
+            check(h, rows[i * n_req:(i + 1) * n_req], have, [1] * n_req, ("replayed", i))
+            have = [x + 1 for x in have]
+    finally:
+        pair.close()
+
+
+def test_block_over_a_paged_cache_refuses():
+    import oracle as O
+    from llama_decoder_block_kv_b200 import synth
+    from tests.gpu_util import Pair
+
+    w = synth.Workload(name="paged block refusals", dim=256, n_layers=1, n_heads=4, n_kv_heads=2, ffn_hidden=O.ffn_hidden_dim(256, 256),
+                       vocab_size=0, multiple_of=256, ffn_dim_multiplier=None, norm_eps=1e-5, rope_theta=10000.0, max_batch_size=1,
+                       max_seq_len=64, act="bf16", batch=1, seed=9, norm_weights="random")
+    pair = Pair(w)
+    try:
+        a = B.PageArgs(4, 2, 64, 16, 4, 4)
+        x = dict(h=torch.zeros((2, 256), device="cuda"), kp=torch.zeros((4, 2, 16, 64), dtype=torch.bfloat16, device="cuda"),
+                 table=ints([[0, 1, 2, 3]]), cu=ints([0, 2]), kv=ints([2]), pos=ints([0, 1]), slot=ints([0, 1]),
+                 ws=torch.zeros(B.llama_block_paged_workspace_bytes(pair.ctx, 2), dtype=torch.uint8, device="cuda"), st=status_word())
+
+        def call(layer=0, a=a, max_new=2, **kw):
+            y = x | kw
+            B.llama_block_forward_paged(pair.ctx, layer, y["h"], a, y["kp"], y["kp"].clone(), y["table"], y["cu"], y["kv"], y["pos"],
+                                        y["slot"], max_new, y["ws"], y["st"])
+
+        call()
+        for kw in (dict(layer=1), dict(layer=-1), dict(max_new=0), dict(ws=x["ws"][:-256])):
+            with pytest.raises(B.LlamaError):
+                call(**kw)
+        for bad in (dict(n_heads=8), dict(n_kv_heads=4), dict(dtype="fp32")):
+            y = dict(n_heads=4, n_kv_heads=2, head_dim=64, page_size=16, num_pages=4, max_pages=4, dtype="bf16") | bad
+            b = B.PageArgs(**y)
+            kp = torch.zeros((4, b.n_kv_heads, 16, 64), dtype=DT[b.dtype], device="cuda")
+            with pytest.raises((B.LlamaError, ValueError)):
+                call(a=b, kp=kp)
+        with pytest.raises(ValueError):
+            call(h=x["h"].double())
+        # positions past the context's max_seq_len are flagged, not appended
+        call(pos=ints([0, 64]))
+        assert B.llama_paged_status(x["st"]) == (B.LLAMA_ERR_POS_RANGE, 2)
+    finally:
+        pair.close()
