@@ -70,7 +70,7 @@ struct RtCfg {
   static constexpr uint32_t TILE = HALVES * HALF;        // a Q tile or a K or V stage
   static constexpr int STAGES = 131072 / TILE;           // 128 KB of ring
   static constexpr uint32_t S_COL = 0, O_COL = 256;      // S/P of A, B at 0, 128; O of A, B at 256, 384
-  static constexpr int BARS = 2 * STAGES + 21 + 2 * RT_SEGS;
+  static constexpr int BARS = 2 * STAGES + 17 + 2 * RT_SEGS;
   static constexpr uint32_t OUT = 4096;                  // a softmax warp's 32 rows x 64 bf16 on their way out
   static constexpr size_t SMEM = 1024 + 2 * TILE + STAGES * TILE + 8 * OUT + BARS * 8 + 16 + RT_SEGS * sizeof(RtSeg) + 8 +
                                  (RT_PRE + 1) * 8;
@@ -193,8 +193,8 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
   uint64_t* p_full = s_full + 2;       // [2 g + part] P of the first 96 / last 32 keys written over S
   uint64_t* o_full = p_full + 4;       // [g] the segment's last P V has finished
   uint64_t* o_free = o_full + 2;       // [g] O has been read
-  uint64_t* turn = o_free + 2;         // [4 g + quarter] the other tile's warp has taken its exponentials
-  uint64_t* g_full = turn + 8;         // [RT_SEGS] segment k is described in segs[k % RT_SEGS]
+  volatile int* turns = reinterpret_cast<volatile int*>(o_free + 2);  // [4 g + quarter] key tiles whose exponentials are taken
+  uint64_t* g_full = o_free + 6;        // [RT_SEGS] segment k is described in segs[k % RT_SEGS]
   uint64_t* g_empty = g_full + RT_SEGS;  // its readers (a warp each) have left it
   uint64_t* meet = g_empty + RT_SEGS;  // the softmax warps, at a cut unit
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(meet + 1);
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     mbar_init(q_full, 1);
     mbar_init(q_empty, 2);
     for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 128);
-    for (int i = 0; i < 8; ++i) mbar_init(&turn[i], 32);
+    for (int i = 0; i < 8; ++i) turns[i] = 0;
     mbar_init(meet, 256);
     for (int i = 0; i < RT_SEGS; ++i) {
       mbar_init(&g_full[i], 1);
@@ -449,10 +449,13 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     bool ok = true;
     // The warps of A and B on one scheduler take their exponentials in turn: A's tile
     // n after B's n - 1, B's n after A's n. Left alone they fall into step, both at the
-    // exponentials and then both waiting for the tensor core.
+    // exponentials and then both waiting for the tensor core. No more than a hint: a
+    // warp that has waited long goes on.
     auto my_turn = [&] {
-      if (g == 1 || n > 0) ok = wait_or_abort(&turn[4 * g + quarter], (g == 1 ? n : n - 1) & 1, p.status, abort_flag);
-      ok = __all_sync(0xffffffffu, ok);
+      const int want = g == 0 ? n : n + 1;
+      for (int i = 0; i < 256 && turns[4 * (g ^ 1) + quarter] < want; ++i) {
+      }
+      __syncwarp();
     };
     int met = 0;
     auto meet_all = [&] {
@@ -460,9 +463,9 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
       ok = wait_or_abort(meet, met++ & 1, p.status, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
     };
-    auto pass_turn = [&] {
-      mbar_arrive(&turn[4 * (g ^ 1) + quarter]);
-      ++n;
+    auto pass_turn = [&](int tiles) {
+      n += tiles;
+      turns[4 * g + quarter] = n;
     };
     for (int seg = 0; __all_sync(0xffffffffu, enter(seg)); ++seg) {
       const RtSeg& w = segs[seg % RT_SEGS];
@@ -472,12 +475,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
       const int last = min(w.s.kv - w.s.n_new + min(tok, w.s.n_new - 1), w.s.kv - 1);
       const bool live = __any_sync(0xffffffffu, tok < w.s.n_new);  // else no row of this warp is anyone's
       float m_used = -INFINITY, l = 0.f;
-      for (int j = w.j0; ok && j < j1; ++j) {
-        if (j >= jl) {
-          my_turn();
-          pass_turn();
-          continue;
-        }
+      for (int j = w.j0; ok && j < jl; ++j) {
         ok = wait_or_abort(&s_full[g], sc & 1, p.status, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -550,7 +548,6 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
             rt_st16(s_cols + c0 / 2, pp);
           };
           my_turn();
-          if (!ok) break;
           weights(0);
           weights(32);
           weights(64);
@@ -558,7 +555,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
           tc_fence_before();
           mbar_arrive(&p_full[2 * g]);
           weights(96);
-          pass_turn();
+          pass_turn(1);
           float a0, a1, b0, b1;
           rt_split(ls[0], a0, a1);
           rt_split(ls[1], b0, b1);
@@ -566,12 +563,12 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
           rt_st_wait();
           tc_fence_before();
         } else {
-          my_turn();
-          pass_turn();
+          pass_turn(1);
           mbar_arrive(&p_full[2 * g]);
         }
         mbar_arrive(&p_full[2 * g + 1]);
       }
+      pass_turn(j1 - max(jl, w.j0));
       const bool work = w.j0 < jl;
       if (ok && work) {
         ok = wait_or_abort(&o_full[g], oc & 1, p.status, abort_flag);
