@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     int sc = 0, oc = 0;                // S tiles taken, segments with work
     int n = 0;                         // key tiles walked (ring slots 2 n, 2 n + 1)
     bool ok = true;
-    // The warps of A and B on one scheduler take their exponentials in turn: A's tile
+    // The warps of A and B on one scheduler take maximum and exponentials in turn: A's tile
     // n after B's n - 1, B's n after A's n. Left alone they fall into step, both at the
     // exponentials and then both waiting for the tensor core. No more than a hint: a
     // warp that has waited long goes on.
@@ -500,11 +500,12 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
 #pragma unroll
           for (int c = 0; c < RT_KT; c += 32) rt_ld32(s_cols + c, s + c);
           rt_ld_wait<RT_KT>(s);
-          if (__any_sync(0xffffffffu, key0 + RT_KT - 1 > last)) {
+          const int seen = last - key0;  // keys 0 .. seen of the tile
+          if (__any_sync(0xffffffffu, RT_KT - 1 > seen)) {
 #pragma unroll
-            for (int c = 0; c < RT_KT; ++c)
-              if (key0 + c > last) s[c] = -INFINITY;
+            for (int c = 0; c < RT_KT; ++c) s[c] = c > seen ? -INFINITY : s[c];
           }
+          my_turn();
           float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
           for (int c = 4; c < RT_KT - 4; c += 8)
@@ -547,7 +548,6 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
             }
             rt_st16(s_cols + c0 / 2, pp);
           };
-          my_turn();
           weights(0);
           weights(32);
           weights(64);
@@ -593,23 +593,27 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
             rt_ld32(o_cols + c, ov);
             rt_ld32(o_cols + c + 32, ov + 32);
             rt_ld_wait<64>(ov);
-            if (lane == 0) rt_store_wait_read();  // the box before has been read
-            __syncwarp();
+            if (c + 64 >= D) {
+              tc_fence_before();
+              mbar_arrive(&o_free[g]);
+            }
+            uint4 u[8];
 #pragma unroll
             for (int e = 0; e < 64; ++e) {
               ov[e] = last < 0 ? 0.f : ov[e] * inv;
               bad |= !(fabsf(ov[e]) < INFINITY);
             }
 #pragma unroll
-            for (int e = 0; e < 64; e += 8)
-              store8(reinterpret_cast<bf16*>(out + lane * 128 + (((e >> 3) ^ (lane & 7)) << 4)), ov + e);
+            for (int e = 0; e < 8; ++e) store8(reinterpret_cast<bf16*>(&u[e]), ov + 8 * e);
+            if (lane == 0) rt_store_wait_read();  // the box before has been read
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(out + lane * 128 + ((e ^ (lane & 7)) << 4)) = u[e];
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
               rt_store_3d(&map_o, out, c, w.h0, w.s.q0 + w.tok0 + g * bh + tok_end - 31 / hpc);
           }
-          tc_fence_before();
-          mbar_arrive(&o_free[g]);
           if (__any_sync(0xffffffffu, bad)) {
             if (lane == 0) rt_store_wait();  // before those rows are written again
             __syncwarp();
