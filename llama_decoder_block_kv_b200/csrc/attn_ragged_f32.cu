@@ -71,34 +71,41 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
   rt_start<RF_KT>(p, pre, HG, bq, w);
   for (; rt_segment<RF_KT>(bq, w); rt_advance(p, HG, bq, w)) {
     const int kvh = w.zl / groups, h0 = kvh * n_rep + (w.zl - kvh * groups) * hpc, tok0 = w.t * bq;
+    // a thread copies 16 bytes of the same column of every LR-th row
+    constexpr int LR = RF_THREADS * 4 / D;
+    const int lrow = tid / (D / 4), lcol = (tid % (D / 4)) * 4;
     auto load = [&](float* dst, int ld, const void* src, long long row_stride, int j) {
-#pragma unroll 4
-      for (int e = tid; e < RF_KT * D / 4; e += RF_THREADS) {
-        const int r = e / (D / 4), c = (e - r * (D / 4)) * 4, key = j * RF_KT + r;
+      const float* from = static_cast<const float*>(src) + lcol;
+      const int* table = p.tables + (size_t)w.b * p.max_pages;
+#pragma unroll 8
+      for (int i = 0; i < RF_KT / LR; ++i) {
+        const int r = lrow + i * LR, key = j * RF_KT + r;
         bool have = key < w.s.kv;
-        size_t at = 0;
+        const float* at = from;
         if (p.tables) {
-          if (have) {
-            const int page = __ldg(p.tables + (size_t)w.b * p.max_pages + (key >> p.page_shift));
-            have = (unsigned)page < (unsigned)p.num_pages;
-            if (have)
-              at = (((((size_t)page * p.Hkv + kvh) << p.page_shift) + (key & ((1 << p.page_shift) - 1))) * D) + c;
-            else
-              atomicOr(p.status, LLAMA_DEV_PAGE_RANGE);
+          const int page = have ? __ldg(table + (key >> p.page_shift)) : 0;
+          if ((unsigned)page >= (unsigned)p.num_pages) {
+            have = false;
+            atomicOr(p.status, LLAMA_DEV_PAGE_RANGE);
           }
+          // rows of all pages number fewer than 2^31
+          const int row = ((page * p.Hkv + kvh) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+          if (have) at += (size_t)row * D;
         } else if (have) {
-          at = (size_t)(w.s.q0 + key) * row_stride + (size_t)kvh * D + c;
+          at += (size_t)(w.s.q0 + key) * row_stride + kvh * D;
         }
-        rf_copy16(dst + r * ld + c, static_cast<const float*>(src) + at, have ? 16 : 0);
+        rf_copy16(dst + r * ld + lcol, at, have ? 16 : 0);
       }
       rf_commit();
     };
     __syncthreads();  // shared memory of the segment before has been read
-    for (int e = tid; e < RF_ROWS * D / 4; e += RF_THREADS) {
-      const int r = e / (D / 4), c = (e - r * (D / 4)) * 4, tok = tok0 + r / hpc;
+#pragma unroll
+    for (int i = 0; i < RF_ROWS / LR; ++i) {
+      const int r = lrow + i * LR, tok = tok0 + r / hpc;
       const bool have = tok < w.s.n_new;
-      const size_t at = have ? (size_t)(w.s.q0 + tok) * p.q_stride + (size_t)(h0 + r % hpc) * D + c : 0;
-      rf_copy16(sQ + r * LD + c, static_cast<const float*>(p.q) + at, have ? 16 : 0);
+      const float* at = static_cast<const float*>(p.q) + lcol;
+      if (have) at += (size_t)(w.s.q0 + tok) * p.q_stride + (h0 + r % hpc) * D;
+      rf_copy16(sQ + r * LD + lcol, at, have ? 16 : 0);
     }
     load(sK, LD, p.k, p.k_stride, w.j0);
     load(sV, D, p.v, p.v_stride, w.j0);

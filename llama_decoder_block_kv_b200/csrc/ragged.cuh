@@ -88,31 +88,34 @@ __device__ void ragged_row(const RaggedAttnParams& p, int b, const RaggedSeq& s,
 constexpr int RT_PRE = 128;  // prefix sums kept, at equal distances over the requests
 constexpr int RT_UNIT = 1;
 
+// bq and KT are powers of two: no divisions (64-bit ones took most of a small call's start)
+__device__ __forceinline__ int rt_log2(int x) { return 31 - __clz(x); }
+__device__ __forceinline__ int rt_blocks(int n_new, int bq) { return (n_new + bq - 1) >> rt_log2(bq); }
 // q tile t of a request: its key tiles; the sum over the tiles before it (all full)
 template <int KT>
-__host__ __device__ __forceinline__ int rt_tiles(int c, int n_new, int bq, int t) {
+__device__ __forceinline__ int rt_tiles(int c, int n_new, int bq, int t) {
   const long long last = min((long long)(t + 1) * bq, (long long)n_new);
   return (int)((c + last + KT - 1) / KT);
 }
-__host__ __device__ __forceinline__ long long rt_floor_sum(long long m, int r) {  // sum of i / r over i < m
-  const long long q = m / r;
-  return r * (q * (q - 1) / 2) + q * (m - q * r);
+__device__ __forceinline__ long long rt_floor_sum(long long m, int lr) {  // sum of i >> lr over i < m
+  const long long q = m >> lr;
+  return ((q * (q - 1) / 2) << lr) + q * (m - (q << lr));
 }
 template <int KT>
-__host__ __device__ __forceinline__ long long rt_before(int c, int bq, long long t) {
+__device__ __forceinline__ long long rt_before(int c, int bq, long long t) {
   if (bq >= KT) {
-    const int s = bq / KT;
+    const int s = bq >> rt_log2(KT);
     return t * (((long long)c + KT - 1) / KT) + s * (t * (t + 1) / 2);
   }
-  // ceil((c + (i + 1) bq) / 128) = floor((e + i) / r) + 1 with e = ceil(c / bq), r = 128 / bq
-  const int r = KT / bq;
-  const long long e = ((long long)c + bq - 1) / bq;
-  return t + rt_floor_sum(e + t, r) - rt_floor_sum(e, r);
+  // ceil((c + (i + 1) bq) / KT) = floor((e + i) / r) + 1 with e = ceil(c / bq), r = KT / bq
+  const int lr = rt_log2(KT) - rt_log2(bq);
+  const long long e = ((long long)c + bq - 1) >> rt_log2(bq);
+  return t + rt_floor_sum(e + t, lr) - rt_floor_sum(e, lr);
 }
 template <int KT>
-__host__ __device__ __forceinline__ long long rt_total(int c, int n_new, int bq) {
+__device__ __forceinline__ long long rt_total(int c, int n_new, int bq) {
   if (n_new <= 0) return 0;
-  const int nt = (n_new + bq - 1) / bq;
+  const int nt = rt_blocks(n_new, bq);
   return rt_before<KT>(c, bq, nt - 1) + rt_tiles<KT>(c, n_new, bq, nt - 1) + (long long)RT_UNIT * nt;
 }
 __host__ __device__ __forceinline__ long long rt_begin(long long c, long long W, long long G) { return c * W / G; }
@@ -134,7 +137,7 @@ struct RtWalk {
 __device__ __forceinline__ void rt_load(const RaggedAttnParams& p, int bq, RtWalk& w) {
   ragged_seq(p, w.b, w.s, false);
   w.c = max(w.s.kv - w.s.n_new, 0);
-  w.nt = (w.s.n_new + bq - 1) / bq;
+  w.nt = rt_blocks(w.s.n_new, bq);
 }
 // to entry w.x; pre[i]: entries of one head group of the requests before i * per
 template <int KT>
@@ -152,7 +155,7 @@ __device__ __forceinline__ void rt_start(const RaggedAttnParams& p, const long l
     if (off < per * HG || w.b == p.B - 1) break;
     off -= per * HG;
   }
-  w.zl = (int)(off / per);
+  w.zl = off < (1LL << 31) && per < (1LL << 31) ? (int)((unsigned)off / (unsigned)per) : (int)(off / per);
   off -= w.zl * per;
   int a = 0, z = w.nt - 1;
   while (a < z) {
