@@ -372,8 +372,12 @@ class PageArgs:
                              self.head_dim, self.page_size, self.num_pages, self.max_pages)
 
 
-def _raw_stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+# The current stream as an address, without a Stream object around it (0.1 us against 3.3: a fifth of a small call)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
+def _raw_stream(stream, device: int) -> int:
+    return _current_raw_stream(device) if stream is None else stream.cuda_stream
 
 
 def _on_device(name: str, t: torch.Tensor, dtype, device: int) -> int:
@@ -424,7 +428,7 @@ def llama_page_plan(args: PageArgs, cached_lens: torch.Tensor, new_lens: torch.T
         _whole("free_pages", free_pages, i32, (args.num_pages,), d), _whole("free_count", free_count, i32, (1,), d),
         _whole("free_count_out", free_count_out, i32, (1,), d), _whole("cu", cu, i32, (n + 1,), d),
         _whole("kv_lens", kv_lens, i32, (n,), d), _whole("positions", positions, i32, (T,), d),
-        _whole("slots", slots, i32, (T,), d), _whole("status", status, i32, (1,), d), _raw_stream(stream)), "llama_page_plan")
+        _whole("slots", slots, i32, (T,), d), _whole("status", status, i32, (1,), d), _raw_stream(stream, d)), "llama_page_plan")
 
 
 def llama_rope_append(args: PageArgs, qkv: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
@@ -445,7 +449,7 @@ def llama_rope_append(args: PageArgs, qkv: torch.Tensor, positions: torch.Tensor
         _whole("positions", positions, i32, (n,), d), _whole("slots", slots, i32, (n,), d), n,
         _whole("rope", rope, torch.float32, (-1, D // 2, 2), d), rope.shape[0],
         _whole("q_out", q_out, dt, (n, args.n_heads, D), d), _whole("k_pages", k_pages, dt, pool, d),
-        _whole("v_pages", v_pages, dt, pool, d), _whole("status", status, i32, (1,), d), _raw_stream(stream)),
+        _whole("v_pages", v_pages, dt, pool, d), _whole("status", status, i32, (1,), d), _raw_stream(stream, d)),
         "llama_rope_append")
 
 
@@ -470,7 +474,7 @@ def llama_attn_paged(args: PageArgs, q: torch.Tensor, k_pages: torch.Tensor, v_p
         _whole("block_tables", block_tables, i32, (B, args.max_pages), d), _whole("cu", cu, i32, (B + 1,), d),
         _whole("kv_lens", kv_lens, i32, (B,), d), B, n, int(max_new), _whole("out", out, dt, (n, args.n_heads, D), d),
         _whole("workspace", workspace, torch.uint8, (-1,), d), workspace.shape[0],
-        _whole("status", status, i32, (1,), d), _raw_stream(stream)), "llama_attn_paged")
+        _whole("status", status, i32, (1,), d), _raw_stream(stream, d)), "llama_attn_paged")
 
 
 def llama_attn_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, max_len: int,
@@ -488,7 +492,7 @@ def llama_attn_packed(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: tor
     _check(lib().llama_attn_packed(
         _CODE[dt], H, Hkv, D, qp, qs, kp, ks, vp, vs, _whole("cu", cu, i32, (-1,), d), cu.shape[0] - 1, n, int(max_len),
         _whole("out", out, dt, (n, H, D), d), _whole("workspace", workspace, torch.uint8, (-1,), d), workspace.shape[0],
-        _whole("status", status, i32, (1,), d), _raw_stream(stream)), "llama_attn_packed")
+        _whole("status", status, i32, (1,), d), _raw_stream(stream, d)), "llama_attn_packed")
 
 
 def llama_block_paged_workspace_bytes(ctx, n_tokens: int) -> int:
@@ -513,7 +517,7 @@ def llama_block_forward_paged(ctx, layer: int, h: torch.Tensor, args: PageArgs, 
         _whole("cu", cu, i32, (B + 1,), d), _whole("kv_lens", kv_lens, i32, (B,), d),
         _whole("positions", positions, i32, (n,), d), _whole("slots", slots, i32, (n,), d), B, n, int(max_new),
         _whole("workspace", workspace, torch.uint8, (-1,), d), workspace.shape[0], _whole("status", status, i32, (1,), d),
-        _raw_stream(stream)), "llama_block_forward_paged")
+        _raw_stream(stream, d)), "llama_block_forward_paged")
 
 
 def llama_paged_status(status: torch.Tensor):

@@ -668,3 +668,79 @@ def test_block_over_a_paged_cache_refuses():
         assert B.llama_paged_status(x["st"]) == (B.LLAMA_ERR_POS_RANGE, 2)
     finally:
         pair.close()
+
+
+# ------------------------------------------------------------------ far pages, shared pages, the most requests
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n", [1, 40])
+def test_pages_far_into_a_large_pool(n, dtype):
+    """Pools of more than 2^32 elements (and 2^33 bytes): rows past every 32-bit offset are appended to and read."""
+    H, Hkv, D, page = 8, 4, 128, 128
+    P = (2 ** 32 // (Hkv * page * D)) + 70
+    a = B.PageArgs(H, Hkv, D, page, P, 4, dtype)
+    kp, vp = (torch.empty((P, Hkv, page, D), dtype=DT[dtype], device="cuda") for _ in range(2))
+    ids = [P - 1, 3, P - 2]
+    kv = 300
+    for x in (kp, vp):
+        x[ids] = float("nan")
+    slots = [ids[j // page] * page + j % page for j in range(kv)]
+    qkv, cs = normal((kv, (H + 2 * Hkv) * D), torch.float32, 4), rope_table(kv, D)
+    q = torch.empty((kv, H, D), dtype=DT[dtype], device="cuda")
+    st = status_word()
+    B.llama_rope_append(a, qkv, ints(list(range(kv))), ints(slots), cs, q, kp, vp, st)
+    x = qkv.double().view(kv, H + 2 * Hkv, D)
+    k, v = (R.gather(p, ids, kv) for p in (kp, vp))
+    step = 2.0 ** -7 if dtype == "bf16" else 2.0 ** -20  # either side of a tie
+    turned = R.rope(x[:, H: H + Hkv], cs[:, None])
+    assert ((k - turned).abs() <= step * turned.abs() + 1e-6).all()
+    assert torch.equal(v, x[:, H + Hkv:].to(DT[dtype]).double())
+    out = torch.empty((n, H, D), dtype=DT[dtype], device="cuda")
+    B.llama_attn_paged(a, q[kv - n:], kp, vp, ints([ids + [-1]]), ints([0, n]), ints([kv]), n, out, workspace(H, Hkv, D, dtype), st)
+    assert B.llama_paged_status(st) == (B.LLAMA_OK, 0)
+    check_attention(out, [(0, q[kv - n:], k.to(DT[dtype]), v.to(DT[dtype]))], DT[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n", [1, 20])
+def test_requests_that_share_pages(n, dtype):
+    """Requests with a common prefix list the same pages."""
+    p = Paged([(n, 150), (n, 170), (n, 96)], 8, 2, 128, 32, dtype)
+    t = p.table.tolist()
+    for b in (1, 2):
+        t[b][:2] = t[0][:2]
+    p.table = ints(t)
+    k0, v0 = p.seqs[0][2][:64], p.seqs[0][3][:64]
+    p.seqs = [(s, q, torch.cat([k0, k[64:]]), torch.cat([v0, v[64:]])) for s, q, k, v in p.seqs]
+    p.call()
+    p.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("single", [True, False])
+def test_the_most_requests(single, dtype):
+    """LLAMA_MAX_SEQS requests, most of them without a new token, the last one with."""
+    r = random.Random(6)
+    lens = [((1 if single else r.choice([1, 2, 70])) if b % 41 == 0 or b == B.LLAMA_MAX_SEQS - 1 else 0, 0) for b in range(B.LLAMA_MAX_SEQS)]
+    lens = [(n, n + r.choice([0, 1, 16, 130])) if n else (0, r.choice([0, 5])) for n, _ in lens]
+    p = Paged(lens, 2, 1, 64, 16, dtype)
+    p.call()
+    p.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_a_call_on_another_stream(dtype):
+    """The stream argument is the stream of the work: it waits there for what comes before it."""
+    p = Paged([(1, 300), (30, 90)], 8, 2, 128, 16, dtype)
+    want = p.call().clone()
+    p.out.fill_(LEFT)
+    q = p.wide.clone()
+    p.wide.zero_()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        p.wide.copy_(q)
+    p.call(stream=s)
+    s.synchronize()
+    assert torch.equal(p.out, want)
