@@ -17,6 +17,10 @@
 //               a segment the four states merge in the ring stage of its last tile.
 // V rows past the last key hold whatever the page holds, and 0 x NaN is NaN in the
 // MMA: the warp that owns them zeroes them in shared memory first.
+//
+// Measured: 32 requests of 1024..8128 tokens at 32/8 heads (497 MB) 89 us, 5.6 TB/s, 85 %
+// of a copy; one request of some 600 tokens at 32 heads 9.4 us, bound by the chain
+// lengths, table, tiles, partials, merge.
 #include "ragged.cuh"
 
 #include <algorithm>

@@ -14,6 +14,11 @@
 // shared memory serves 8 products. K(j + 1) is copied while P(j) V(j) runs and V(j + 1)
 // while the scores of j + 1 are taken (cp.async; keys past the last one are zeros).
 //
+// Measured at 4/2 heads of 64: 7 prompts of 5..509 tokens 28.9 us, 5 requests of up to
+// 761 keys with up to 61 new tokens 17.9 us; of a CTA's 15 us there 5 pass before it
+// knows its range and 3 until its first tile is in, the rest is one or two tiles and the
+// merge of the cut unit.
+//
 // A V row of a later key that is not finite reaches the earlier rows of its tile (0 x
 // NaN): rows whose result is not finite are computed again, key by key.
 #include "ragged.cuh"

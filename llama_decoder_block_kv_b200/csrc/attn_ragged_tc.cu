@@ -10,21 +10,46 @@
 // largest power of two up to 8 dividing n_rep) x 256 / hpc positions, as two
 // tiles A and B of 128 rows. It walks the 128-key tiles up to its last
 // position. The tiles of all units, unit-major, form one list that is cut into
-// equal contiguous ranges, one per CTA and one CTA per SM, so the CTAs finish
-// together whatever the lengths; a unit cut between CTAs leaves unnormalised
-// partials (max, sum, O), merged in CTA order by the CTA that arrives last.
+// equal contiguous ranges (ragged.cuh), one per CTA and one CTA per SM, so the
+// CTAs finish together whatever the lengths; a unit cut between CTAs leaves
+// unnormalised partials (max, sum, O), merged in CTA order by the CTA that
+// arrives last.
 //   warp 0      TMA: Q (two boxes of 128 rows), then K(j), V(j) in turn through
 //               a ring of 128-key stages (128-byte swizzle, no multicast); a
 //               stage is 128 / page_size page boxes, a lane each. Pages past
 //               the request's last one are read as out of range, i.e. zeros;
-//   warp 1      one thread issues the MMAs: for each key tile, for A then B:
-//               O += P V (P from TMEM, where the softmax wrote it over S), then
-//               the next S = Q K^T. MMAs of one thread run in order, so S may
+//   warps 1, 2  one thread each issues the MMAs of tile A / B: S = Q K(j)^T,
+//               then O += P V in two parts (P of the first 96 and of the last
+//               32 keys, read from TMEM, where the softmax wrote it over S),
+//               then the next S. MMAs of one thread run in order, so S may
 //               overwrite the P that the MMA before it reads, and the commit
 //               behind S also tells the softmax that O is at rest;
+//   warp 3      finds the CTA's segments in the list, a few ahead;
 //   warps 4..7  softmax of tile A, one thread per row (its TMEM lane);
 //   warps 8..11 softmax of tile B. While one tile's softmax runs, the tensor
 //               core works on the other's.
+//
+// What bounds it: at long prompts the chain of one tile, S -> softmax -> P V ->
+// next S. The MMAs of a 128 x 128 tile take 1029 cycles (64 each, measured) and
+// its exponentials 1024 on the special-function unit (16 a cycle), but from the
+// last MMA of a group to its commit pass another 420 cycles, so a tile's chain
+// is about 1000 cycles of tensor core and 1700 of softmax, and A and B together
+// reach 2500 to 3000 cycles per pair of tiles where the MMAs alone would take
+// 2057. One prompt of 8192 tokens at 32/8 heads of 128: 464 us, 1185 TFLOP/s.
+// Short prompts add what a unit costs besides its tiles (Q, the first S, the
+// last P V, the way out of O: about 5 us, partly under its neighbours' work):
+// 16 prompts of 17..2047 tokens at 32 heads 285 us. Measured on the way:
+//  - one issuing thread picked by its lane number in place of elect.sync, and
+//    one for both tiles: 635 us for the long prompt, 8 MMAs taking 423 cycles
+//    to issue;
+//  - 64-key steps with two S buffers a tile, so that S is never waited for: the
+//    64-wide S MMAs read A as often and cost as much as 128-wide ones (529 us);
+//  - two threads a row (16 softmax warps): 687 us;
+//  - no turns at the exponentials: 655 us, both tiles falling into step;
+//  - a quarter or half of the exponentials by a polynomial on the FMA pipe:
+//    515 and 562 us against 509;
+//  - rows stored by their own threads: 509 us against 484.
+//
 // A thread raises its running maximum only when a score passes it by more than
 // 2^8 (O and the sum are then rescaled), so P <= 2^8.
 //
@@ -248,189 +273,189 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
   // 168 registers a thread at launch; the softmax threads hold a row of S and take
   // what the first four warps give back: 88 + 2 x 208 = 3 x 168
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  if (warp == 0) {
-    // ------------------------------------------------------------------ producer
-    if (lane == 0) {
-      prefetch_tensormap(&map_q);
-      prefetch_tensormap(&map_k);
-      prefetch_tensormap(&map_v);
-    }
-    int i = 0, seg = 0;
-    bool ok = true;
-    while (ok && __all_sync(0xffffffffu, enter(seg))) {
-      const RtSeg& w = segs[seg % RT_SEGS];
-      const int kvh = w.kvh;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == 0) {
+      // ------------------------------------------------------------------ producer
       if (lane == 0) {
-        ok = wait_or_abort(q_empty, (seg & 1) ^ 1, p.status, abort_flag);
-        if (ok) {
-          const int tiles = w.lim[1] ? 2 : 1;
-          mbar_arrive_expect_tx(q_full, tiles * Cfg::TILE);
-          for (int g = 0; g < tiles; ++g)
-#pragma unroll
-            for (int hf = 0; hf < Cfg::HALVES; ++hf)
-              rt_tma_3d(sQ + g * Cfg::TILE + hf * Cfg::HALF, &map_q, q_full, hf * 64, w.h0,
-                        w.s.q0 + w.tok0 + g * bh);
-        }
+        prefetch_tensormap(&map_q);
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
       }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-      // lane -> (64-wide half, page of the tile); one box per lane
-      const int ps = PAGED ? 1 << p.page_shift : RT_KT, boxes = Cfg::HALVES * (RT_KT / ps);
-      const int hf = lane % Cfg::HALVES, pg = lane / Cfg::HALVES;
-      const int n_pages = PAGED ? (w.s.kv + ps - 1) >> p.page_shift : 0;
-      for (int j = w.j0; ok && j < w.j1; ++j) {
-        int row = 0;
-        if (PAGED && lane < boxes) {
-          const int k = j * (RT_KT / ps) + pg;
-          row = p.num_pages * p.Hkv * ps;  // out of range: zeros
-          if (k < n_pages) {
-            const int page = __ldg(p.tables + (size_t)w.b * p.max_pages + k);
-            if ((unsigned)page < (unsigned)p.num_pages)
-              row = (page * p.Hkv + kvh) * ps;
-            else
-              atomicOr(p.status, LLAMA_DEV_PAGE_RANGE);
-          }
-        }
-#pragma unroll
-        for (int kv = 0; kv < 2 && ok; ++kv, ++i) {
-          const int st = i % ST;
-          ok = wait_or_abort(&kv_empty[st], ((i / ST) & 1) ^ 1, p.status, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], Cfg::TILE);
-          __syncwarp();
-          if (lane < boxes) {
-            uint8_t* dst = sKV + st * Cfg::TILE + hf * Cfg::HALF + pg * ps * 128;
-            const CUtensorMap* map = kv ? &map_v : &map_k;
-            if (PAGED)
-              tma_load_2d(dst, map, &kv_full[st], hf * 64, row);
-            else
-              rt_tma_3d(dst, map, &kv_full[st], hf * 64, kvh, w.s.q0 + j * RT_KT);
-          }
-        }
-      }
-      __syncwarp();
-      if (lane == 0) leave(seg);
-      ++seg;
-    }
-    // every copy lands before the CTA can retire
-    if (lane == 0) {
-      if (seg > 0) mbar_wait(q_full, (seg - 1) & 1, p.status);
-      for (int k = (i > ST ? i - ST : 0); k < i; ++k) mbar_wait(&kv_full[k % ST], (k / ST) & 1, p.status);
-    }
-  } else if (warp <= 2) {
-    if (elect_one()) {
-      // ------------------------------------------------------------------ MMA issuer of tile A / B
-      constexpr uint32_t idesc_s = make_idesc_bf16(128, RT_KT);
-      constexpr uint32_t idesc_pv = make_idesc_bf16(128, D) | (1u << 16);  // B (= V) N-major
-      const int g = warp - 1;
-      const uint32_t qa = smem_u32(sQ + g * Cfg::TILE), kv = smem_u32(sKV);
-      const uint32_t sd = tmem + Cfg::S_COL + g * 128, od = tmem + Cfg::O_COL + g * 128;
-      int i = 0, seg = 0;     // ring slots, segments
-      int pc = 0, oc = 0;     // P tiles, segments with work
+      int i = 0, seg = 0;
       bool ok = true;
-      auto wait = [&](uint64_t* bar, uint32_t par) { return ok = ok && wait_or_abort(bar, par & 1, p.status, abort_flag); };
-      auto issue_s = [&](int st) {
-        const uint32_t ka = kv + st * Cfg::TILE;
+      while (ok && __all_sync(0xffffffffu, enter(seg))) {
+        const RtSeg& w = segs[seg % RT_SEGS];
+        const int kvh = w.kvh;
+        if (lane == 0) {
+          ok = wait_or_abort(q_empty, (seg & 1) ^ 1, p.status, abort_flag);
+          if (ok) {
+            const int tiles = w.lim[1] ? 2 : 1;
+            mbar_arrive_expect_tx(q_full, tiles * Cfg::TILE);
+            for (int g = 0; g < tiles; ++g)
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * Cfg::HALF + (kk & 3) * 32;
-          tc_mma_bf16(sd, make_sw128_desc(qa + off), make_sw128_desc(ka + off), idesc_s, kk > 0 ? 1u : 0u);
+              for (int hf = 0; hf < Cfg::HALVES; ++hf)
+                rt_tma_3d(sQ + g * Cfg::TILE + hf * Cfg::HALF, &map_q, q_full, hf * 64, w.h0,
+                          w.s.q0 + w.tok0 + g * bh);
+          }
         }
-        tc_commit(&s_full[g]);
-      };
-      for (; ok && enter(seg); ++seg) {
-        const int j0 = segs[seg % RT_SEGS].j0, j1 = segs[seg % RT_SEGS].j1;
-        const int jl = min(j1, segs[seg % RT_SEGS].lim[g]);  // this tile has work on [j0, jl)
-        leave(seg);
-        if (!wait(q_full, seg) || !wait(&kv_full[i % ST], i / ST)) break;
-        tc_fence_after();
-        if (j0 < jl) {
-          issue_s(i % ST);
-          tc_commit(&kv_empty[i % ST]);
-        } else {
-          mbar_arrive(&kv_empty[i % ST]);
-        }
-        if (jl - j0 <= 1) tc_commit(q_empty);
-        for (int j = j0; j < j1; ++j, i += 2) {
-          const int vs = (i + 1) % ST, ks = (i + 2) % ST;  // ring stages of V(j), K(j + 1)
-          if (!wait(&kv_full[vs], (i + 1) / ST)) break;
-          if (j < jl) {
-            if (j == j0 && !wait(&o_free[g], oc++ ^ 1)) break;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!wait(&p_full[2 * g + h], pc)) break;
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 6 * h; kk < 6 + 2 * h; ++kk)
-                rt_mma_ts(od, sd + kk * 8, rt_desc_n(kv + vs * Cfg::TILE + kk * 2048, Cfg::HALF), idesc_pv,
-                          (j > j0 || kk > 0) ? 1u : 0u);
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+        // lane -> (64-wide half, page of the tile); one box per lane
+        const int ps = PAGED ? 1 << p.page_shift : RT_KT, boxes = Cfg::HALVES * (RT_KT / ps);
+        const int hf = lane % Cfg::HALVES, pg = lane / Cfg::HALVES;
+        const int n_pages = PAGED ? (w.s.kv + ps - 1) >> p.page_shift : 0;
+        for (int j = w.j0; ok && j < w.j1; ++j) {
+          int row = 0;
+          if (PAGED && lane < boxes) {
+            const int k = j * (RT_KT / ps) + pg;
+            row = p.num_pages * p.Hkv * ps;  // out of range: zeros
+            if (k < n_pages) {
+              const int page = __ldg(p.tables + (size_t)w.b * p.max_pages + k);
+              if ((unsigned)page < (unsigned)p.num_pages)
+                row = (page * p.Hkv + kvh) * ps;
+              else
+                atomicOr(p.status, LLAMA_DEV_PAGE_RANGE);
             }
+          }
+#pragma unroll
+          for (int kv = 0; kv < 2 && ok; ++kv, ++i) {
+            const int st = i % ST;
+            ok = wait_or_abort(&kv_empty[st], ((i / ST) & 1) ^ 1, p.status, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            ++pc;
-            if (j + 1 == jl) tc_commit(&o_full[g]);
-          }
-          if (j + 1 < j1) {
-            if (!wait(&kv_full[ks], (i + 2) / ST)) break;
-            if (j + 1 < jl) {
-              issue_s(ks);
-              tc_commit(&kv_empty[ks]);
-            } else {
-              mbar_arrive(&kv_empty[ks]);
+            if (lane == 0) mbar_arrive_expect_tx(&kv_full[st], Cfg::TILE);
+            __syncwarp();
+            if (lane < boxes) {
+              uint8_t* dst = sKV + st * Cfg::TILE + hf * Cfg::HALF + pg * ps * 128;
+              const CUtensorMap* map = kv ? &map_v : &map_k;
+              if (PAGED)
+                tma_load_2d(dst, map, &kv_full[st], hf * 64, row);
+              else
+                rt_tma_3d(dst, map, &kv_full[st], hf * 64, kvh, w.s.q0 + j * RT_KT);
             }
           }
-          if (j < jl)
-            tc_commit(&kv_empty[vs]);
-          else
-            mbar_arrive(&kv_empty[vs]);
-          if (j + 2 == jl) tc_commit(q_empty);  // the segment's last S has been issued
+        }
+        __syncwarp();
+        if (lane == 0) leave(seg);
+        ++seg;
+      }
+      // every copy lands before the CTA can retire
+      if (lane == 0) {
+        if (seg > 0) mbar_wait(q_full, (seg - 1) & 1, p.status);
+        for (int k = (i > ST ? i - ST : 0); k < i; ++k) mbar_wait(&kv_full[k % ST], (k / ST) & 1, p.status);
+      }
+    } else if (warp <= 2) {
+      if (elect_one()) {
+        // ------------------------------------------------------------------ MMA issuer of tile A / B
+        constexpr uint32_t idesc_s = make_idesc_bf16(128, RT_KT);
+        constexpr uint32_t idesc_pv = make_idesc_bf16(128, D) | (1u << 16);  // B (= V) N-major
+        const int g = warp - 1;
+        const uint32_t qa = smem_u32(sQ + g * Cfg::TILE), kv = smem_u32(sKV);
+        const uint32_t sd = tmem + Cfg::S_COL + g * 128, od = tmem + Cfg::O_COL + g * 128;
+        int i = 0, seg = 0;     // ring slots, segments
+        int pc = 0, oc = 0;     // P tiles, segments with work
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t par) { return ok = ok && wait_or_abort(bar, par & 1, p.status, abort_flag); };
+        auto issue_s = [&](int st) {
+          const uint32_t ka = kv + st * Cfg::TILE;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * Cfg::HALF + (kk & 3) * 32;
+            tc_mma_bf16(sd, make_sw128_desc(qa + off), make_sw128_desc(ka + off), idesc_s, kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&s_full[g]);
+        };
+        for (; ok && enter(seg); ++seg) {
+          const int j0 = segs[seg % RT_SEGS].j0, j1 = segs[seg % RT_SEGS].j1;
+          const int jl = min(j1, segs[seg % RT_SEGS].lim[g]);  // this tile has work on [j0, jl)
+          leave(seg);
+          if (!wait(q_full, seg) || !wait(&kv_full[i % ST], i / ST)) break;
+          tc_fence_after();
+          if (j0 < jl) {
+            issue_s(i % ST);
+            tc_commit(&kv_empty[i % ST]);
+          } else {
+            mbar_arrive(&kv_empty[i % ST]);
+          }
+          if (jl - j0 <= 1) tc_commit(q_empty);
+          for (int j = j0; j < j1; ++j, i += 2) {
+            const int vs = (i + 1) % ST, ks = (i + 2) % ST;  // ring stages of V(j), K(j + 1)
+            if (!wait(&kv_full[vs], (i + 1) / ST)) break;
+            if (j < jl) {
+              if (j == j0 && !wait(&o_free[g], oc++ ^ 1)) break;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (!wait(&p_full[2 * g + h], pc)) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 6 * h; kk < 6 + 2 * h; ++kk)
+                  rt_mma_ts(od, sd + kk * 8, rt_desc_n(kv + vs * Cfg::TILE + kk * 2048, Cfg::HALF), idesc_pv,
+                            (j > j0 || kk > 0) ? 1u : 0u);
+              }
+              if (!ok) break;
+              ++pc;
+              if (j + 1 == jl) tc_commit(&o_full[g]);
+            }
+            if (j + 1 < j1) {
+              if (!wait(&kv_full[ks], (i + 2) / ST)) break;
+              if (j + 1 < jl) {
+                issue_s(ks);
+                tc_commit(&kv_empty[ks]);
+              } else {
+                mbar_arrive(&kv_empty[ks]);
+              }
+            }
+            if (j < jl)
+              tc_commit(&kv_empty[vs]);
+            else
+              mbar_arrive(&kv_empty[vs]);
+            if (j + 2 == jl) tc_commit(q_empty);  // the segment's last S has been issued
+          }
+        }
+        // every MMA finishes before TMEM is freed: the softmax warps wait for all of
+        // them (o_full), except after a timeout
+        if (!ok) {
+          tc_commit(q_empty);
+          const uint64_t t0 = global_timer_ns();
+          while (global_timer_ns() - t0 < LLAMA_WAIT_LIMIT_NS / 16) {
+          }
         }
       }
-      // every MMA finishes before TMEM is freed: the softmax warps wait for all of
-      // them (o_full), except after a timeout
-      if (!ok) {
-        tc_commit(q_empty);
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < LLAMA_WAIT_LIMIT_NS / 16) {
+    } else if (lane == 0) {
+      // ------------------------------------------------------------------ scheduler
+      const long long W = pre[RT_PRE] * HG, G = min((long long)gridDim.x, W), cta = blockIdx.x;
+      RtWalk w;
+      w.x = cta < G ? rt_begin(cta, W, G) : 0;
+      w.end = cta < G ? rt_begin(cta + 1, W, G) : 0;
+      const long long xbeg = w.x;
+      rt_start<RT_KT>(p, pre, HG, bq, w);
+      for (int k = 0;; ++k) {
+        const bool more = rt_segment<RT_KT>(bq, w);
+        if (!wait_or_abort(&g_empty[k % RT_SEGS], ((k / RT_SEGS) & 1) ^ 1, p.status, abort_flag)) break;
+        RtSeg& q = segs[k % RT_SEGS];
+        q.j1 = 0;
+        if (more) {
+          q.b = w.b;
+          q.s = w.s;
+          q.tok0 = w.t * bq;
+          q.kvh = w.zl / groups;
+          q.h0 = q.kvh * n_rep + (w.zl - q.kvh * groups) * hpc;
+          q.j0 = w.j0;
+          q.j1 = w.j1;
+          q.whole = w.j0 == 0 && w.j1 == w.n;
+          q.lim[0] = w.lim[0];
+          q.lim[1] = w.lim[1];
+          // a CTA has at most two cut units, one at either end of its range
+          q.slot = (int)(2 * cta + (w.xs <= xbeg ? 0 : 1));
+          const long long x0 = w.xs + RT_UNIT;  // the unit's first tile
+          q.c0 = (int)rt_own(x0, W, G);
+          q.c1 = (int)rt_own(x0 + w.n - 1, W, G);
+          q.slot0 = 2 * q.c0 + (w.xs <= rt_begin(q.c0, W, G) ? 0 : 1);
         }
+        mbar_arrive(&g_full[k % RT_SEGS]);
+        if (!more) break;
+        rt_advance(p, HG, bq, w);
       }
     }
-  } else if (lane == 0) {
-    // ------------------------------------------------------------------ scheduler
-    const long long W = pre[RT_PRE] * HG, G = min((long long)gridDim.x, W), cta = blockIdx.x;
-    RtWalk w;
-    w.x = cta < G ? rt_begin(cta, W, G) : 0;
-    w.end = cta < G ? rt_begin(cta + 1, W, G) : 0;
-    const long long xbeg = w.x;
-    rt_start<RT_KT>(p, pre, HG, bq, w);
-    for (int k = 0;; ++k) {
-      const bool more = rt_segment<RT_KT>(bq, w);
-      if (!wait_or_abort(&g_empty[k % RT_SEGS], ((k / RT_SEGS) & 1) ^ 1, p.status, abort_flag)) break;
-      RtSeg& q = segs[k % RT_SEGS];
-      q.j1 = 0;
-      if (more) {
-        q.b = w.b;
-        q.s = w.s;
-        q.tok0 = w.t * bq;
-        q.kvh = w.zl / groups;
-        q.h0 = q.kvh * n_rep + (w.zl - q.kvh * groups) * hpc;
-        q.j0 = w.j0;
-        q.j1 = w.j1;
-        q.whole = w.j0 == 0 && w.j1 == w.n;
-        q.lim[0] = w.lim[0];
-        q.lim[1] = w.lim[1];
-        // a CTA has at most two cut units, one at either end of its range
-        q.slot = (int)(2 * cta + (w.xs <= xbeg ? 0 : 1));
-        const long long x0 = w.xs + RT_UNIT;  // the unit's first tile
-        q.c0 = (int)rt_own(x0, W, G);
-        q.c1 = (int)rt_own(x0 + w.n - 1, W, G);
-        q.slot0 = 2 * q.c0 + (w.xs <= rt_begin(q.c0, W, G) ? 0 : 1);
-      }
-      mbar_arrive(&g_full[k % RT_SEGS]);
-      if (!more) break;
-      rt_advance(p, HG, bq, w);
-    }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // -------------------------------------------------------------------- softmax
