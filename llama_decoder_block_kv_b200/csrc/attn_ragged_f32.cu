@@ -20,7 +20,8 @@
 // merge of the cut unit.
 //
 // A V row of a later key that is not finite reaches the earlier rows of its tile (0 x
-// NaN): rows whose result is not finite are computed again, key by key.
+// NaN): rows whose result is not finite are computed again, key by key (unless their sum
+// is NaN or zero: then a key they see makes the whole row NaN).
 #include "ragged.cuh"
 
 #include <algorithm>
@@ -48,6 +49,16 @@ __device__ __forceinline__ void rf_copy16(void* dst, const void* src, int bytes)
 }
 __device__ __forceinline__ void rf_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void rf_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
+
+// out of line: in line it costs the kernel registers for a path that hardly runs
+template <int D>
+__device__ __noinline__ void rf_row(const RaggedAttnParams& p, int b, int q0, int n_new, int kv, int tok, int h, int lane) {
+  RaggedSeq s;
+  s.q0 = q0;
+  s.n_new = n_new;
+  s.kv = kv;
+  ragged_row<float, D>(p, b, s, tok, h, lane);
+}
 
 template <int D>
 __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
@@ -233,7 +244,7 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
 #pragma unroll
       for (int c = 0; c < 4 * NC; ++c) {
         o[i][c] = last[i] < 0 ? 0.f : o[i][c] * inv;  // a row without keys is zero
-        bad[i] |= !(fabsf(o[i][c]) < INFINITY);
+        bad[i] |= sum > 0.f && !(fabsf(o[i][c]) < INFINITY);
       }
 #pragma unroll
       for (int c = 0; c < NC; ++c) store4(dst + 64 * c + 4 * tx, o[i] + 4 * c);
@@ -328,7 +339,7 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
         if ((b >> (16 * half)) & 0xffffu) {
           __syncwarp();  // behind the stores above
           const int r = 8 * warp + 4 * half + i;
-          ragged_row<float, D>(p, w.b, w.s, tok0 + r / hpc, h0 + r % hpc, lane);
+          rf_row<D>(p, w.b, w.s.q0, w.s.n_new, w.s.kv, tok0 + r / hpc, h0 + r % hpc, lane);
         }
     }
   }

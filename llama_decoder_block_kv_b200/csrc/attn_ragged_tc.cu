@@ -61,7 +61,8 @@
 // holds; 0 x NaN is NaN in the MMA, so the softmax threads zero those rows of
 // the last tile in shared memory before they hand over P. A V row that is not
 // finite inside the diagonal tile would reach the earlier rows of its tile the
-// same way: rows whose result is not finite are computed again, key by key.
+// same way: rows whose result is not finite are computed again, key by key (unless
+// their sum is NaN or zero: then a key they see makes the whole row NaN).
 #include <algorithm>
 
 #include "ragged.cuh"
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
           tc_fence_before();
           mbar_arrive(&o_free[g]);
         }
-        bad = bad && store;
+        bad = bad && store && l > 0.f;
       } else {
         // partial: O as [D / 4][256 rows] float4, then (max, sum) per row
         float* pp = part + (size_t)w.slot * stride;
@@ -689,6 +690,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
         meet_all();
         if (!ok) break;
         if (*s_last) {
+          float merged = 0.f;  // the row's sum
           // partials of CTAs c0 .. c1 in that order; c0 holds the unit in its second slot
           // unless its range starts inside it, the others in their first
           const int slot0 = w.slot0;
@@ -712,6 +714,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
                 if (v[k].x != -INFINITY) ll += v[k].y * rt_ex2(v[k].x - mm);
             }
             const float inv = last < 0 ? 0.f : 1.f / ll;
+            merged = ll;
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
               float acc[32];
@@ -750,6 +753,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
               for (int e = 0; e < 32; e += 8) store8(dst + d + e, acc + e);
             }
           }
+          bad = bad && merged > 0.f;
           if (tid == RT_LEADER) counters[c0] = 0;  // re-armed for the next launch
         }
         meet_all();  // s_last is written again by the next cut segment

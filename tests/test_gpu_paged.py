@@ -744,3 +744,33 @@ def test_a_call_on_another_stream(dtype):
     p.call(stream=s)
     s.synchronize()
     assert torch.equal(p.out, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_infinite_values_give_what_the_formula_gives(dtype):
+    """V rows with infinities and K rows that make every score -inf or NaN, seen by some rows of a tile and not by
+    others, in whole units and in cut ones: finite, infinite and NaN values stand where the 64-bit form has them."""
+    inf = float("inf")
+    for n, kv, at, what in ((40, 40, 20, "v"), (260, 700, 500, "v"), (40, 300, 280, "k"), (30, 30, 0, "k"), (3, 3000, 2998, "v")):
+        p = Paged([(n, kv), (1, 65)], 8, 2, 128, 16, dtype, seed=3)
+        page, off = int(p.table[0, at // 16]), at % 16
+        t, q, k, v = p.seqs[0]
+        if what == "v":
+            p.vp[page, :, off, ::2] = inf
+            v = v.clone()
+            v[at, :, ::2] = inf
+        else:
+            p.kp[page, :, off, 5] = inf
+            k = k.clone()
+            k[at, :, 5] = inf
+        p.call()
+        assert B.llama_paged_status(p.st) == (B.LLAMA_OK, 0)
+        want, _, _ = R.attention(q, k, v)
+        got = p.out[t:t + n].double()
+        assert torch.equal(torch.isnan(got), torch.isnan(want)), (n, kv, what)
+        assert torch.equal(torch.isinf(got), torch.isinf(want)), (n, kv, what)
+        fine = torch.isfinite(want)
+        # finite values next to infinite ones of the same row: two roundings of the storage type and of P, as the bound's
+        # weights would be infinite too
+        assert ((got - want)[fine].abs() <= 2.0 ** -6 * (want[fine].abs() + 1)).all(), (n, kv, what)
+        check_attention(p.out[n:n + 1], [(0, *p.seqs[1][1:])], p.dt)
