@@ -364,6 +364,8 @@ int llama_selftest_bounded_wait(int which, int* flags, double* seconds);
  * position patterns, the stream-K decode attention's split: every key tile in
  * exactly one CTA's range, each split unit merged from one partial of each CTA
  * it spans, in distinct slots inside the workspace (M up to 1024 there).
+ * The same for the attention over pages and packed prompts, with M requests of
+ * single tokens, chunks, whole prompts and mixtures.
  * Returns LLAMA_OK, LLAMA_ERR_INTERNAL when a check
  * fails, or LLAMA_ERR_INVALID_ARGS for sizes the library rejects. Needs no GPU.
  */

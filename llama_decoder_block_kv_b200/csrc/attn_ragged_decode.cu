@@ -46,19 +46,19 @@ __device__ __forceinline__ float rd_quad_sum(float v) {
   return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-__device__ __forceinline__ long long rd_begin(long long c, long long W, long long G) { return c * W / G; }
-__device__ __forceinline__ long long rd_own(long long x, long long W, long long G) { return ((x + 1) * G - 1) / W; }
+__host__ __device__ __forceinline__ long long rd_begin(long long c, long long W, long long G) { return c * W / G; }
+__host__ __device__ __forceinline__ long long rd_own(long long x, long long W, long long G) { return ((x + 1) * G - 1) / W; }
 
 // tiles of one unit of a request with kv keys (one for a token that sees none: its
 // row is written as zeros), 0 for a request without a new token (kv = -1)
-__device__ __forceinline__ int rd_tiles(int kv) { return kv < 0 ? 0 : kv == 0 ? 1 : (kv - 1) / RD_KT + 1; }
+__host__ __device__ __forceinline__ int rd_tiles(int kv) { return kv < 0 ? 0 : kv == 0 ? 1 : (kv - 1) / RD_KT + 1; }
 
 struct RdUnit {
   int b, zl;  // request, unit inside the request (kv head * groups + group)
   int t;      // tile inside the unit
 };
 // pb[b]: tiles of one head group of the requests before b
-__device__ __forceinline__ RdUnit rd_locate(const long long* pb, const int* kvs, int B, int HG, long long x) {
+__host__ __device__ __forceinline__ RdUnit rd_locate(const long long* pb, const int* kvs, int B, int HG, long long x) {
   int lo = 0, hi = B - 1;  // the last b whose tiles begin at or before x
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -547,6 +547,67 @@ __global__ void __launch_bounds__(160, 2)
 
 static size_t rd_smem(int D, int B) {
   return 1024 + (size_t)RD_STAGES * 2 * RD_KT * D * 2 + 2 * RD_STAGES * 8 + (size_t)(B + 1) * 8 + (size_t)B * 4;
+}
+
+// Host walk of the split, as check_ragged_list
+static bool check_decode_list(const RaggedAttnParams& p, int grid) {
+  const int hpc = decode_heads_per_cta(p.H / p.Hkv), HG = p.H / hpc;
+  if (p.H % hpc) return false;
+  std::vector<long long> pb(p.B + 1, 0);
+  std::vector<int> kvs(p.B);
+  long long units = 0;
+  for (int b = 0; b < p.B; ++b) {
+    RaggedSeq s;
+    ragged_seq(p, b, s, false);
+    kvs[b] = s.n_new ? s.kv : -1;
+    pb[b + 1] = pb[b] + rd_tiles(kvs[b]);
+    units += s.n_new ? HG : 0;
+  }
+  const long long W = pb[p.B] * HG, G = W < grid ? W : grid;
+  std::vector<char> slot_used(2 * (size_t)grid, 0), counter_used(grid, 0);
+  long long done = 0, next = 0;
+  for (int cta = 0; cta < G; ++cta) {
+    const long long sbeg = rd_begin(cta, W, G), send = rd_begin(cta + 1, W, G);
+    if (sbeg != next) return false;
+    next = send;
+    for (long long x = sbeg; x < send;) {
+      const RdUnit u = rd_locate(pb.data(), kvs.data(), p.B, HG, x);
+      const int n = rd_tiles(kvs[u.b]);
+      if (n < 1 || u.zl < 0 || u.zl >= HG || u.t < 0 || u.t >= n || pb[u.b] * HG + (long long)u.zl * n + u.t != x) return false;
+      const long long len = n - u.t < send - x ? n - u.t : send - x, P = x - u.t;
+      if (u.t > 0 || len < n) {
+        const int c0 = (int)rd_own(P, W, G), c1 = (int)rd_own(P + n - 1, W, G), slot = 2 * cta + (P <= sbeg ? 0 : 1);
+        if (cta < c0 || cta > c1 || (u.t == 0) != (cta == c0) || (u.t + len == n) != (cta == c1)) return false;
+        if (slot != (cta == c0 ? 2 * c0 + (rd_begin(c0, W, G) == P ? 0 : 1) : 2 * cta) || slot_used[slot]) return false;
+        slot_used[slot] = 1;
+        if (cta == c0 && counter_used[c0]) return false;
+        counter_used[c0] = 1;
+      }
+      done += u.t + len == n;
+      x += len;
+    }
+  }
+  return next == W && done == units;
+}
+
+// The lists of all three attention kernels for these lengths (host memory), on so many SMs
+bool check_ragged_plans(const int* cu, const int* kv_lens, int B, int N, int max_kv, int H, int Hkv, int num_sms) {
+  RaggedAttnParams p = {};
+  int page = 0;
+  p.cu = cu;
+  p.kv_lens = kv_lens;
+  p.tables = &page;  // lengths as of a paged call
+  p.B = B;
+  p.N = N;
+  p.max_new = N;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.page_shift = 4;
+  p.max_pages = (max_kv + 15) / 16;
+  bool ok = check_ragged_list<128>(p, 256, std::min(num_sms, RAGGED_TC_CTAS));
+  for (int per_sm : {4, 2}) ok = ok && check_ragged_list<64>(p, 32, std::min(num_sms, RAGGED_F32_CTAS / 4) * per_sm);
+  p.max_new = 1;  // requests with more are skipped there
+  return ok && check_decode_list(p, std::min(2 * num_sms, RAGGED_DECODE_CTAS));
 }
 
 size_t ragged_decode_ws_floats(int D) { return (size_t)2 * RAGGED_DECODE_CTAS * rd_part_stride(16, D); }

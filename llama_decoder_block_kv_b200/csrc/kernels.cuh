@@ -238,6 +238,7 @@ constexpr int RAGGED_DECODE_CTAS = 296;  // at most this many CTAs: two per SM
 size_t ragged_decode_ws_floats(int D);
 cudaError_t launch_attn_ragged_decode(const RaggedAttnParams& p, float* part, int* counters, int num_sms,
                                       cudaStream_t st);
+bool check_ragged_plans(const int* cu, const int* kv_lens, int B, int N, int max_kv, int H, int Hkv, int num_sms);
 
 // decode_block.cu: one decode step of a whole block in one persistent launch
 constexpr int DB_RING_STAGES = 9;                 // 16 KB weight tiles in flight per SM

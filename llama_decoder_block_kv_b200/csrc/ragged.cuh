@@ -2,6 +2,8 @@
 // lengths with their checks, and one row computed by a warp, key by key.
 #pragma once
 
+#include <vector>
+
 #include "kernels.cuh"
 
 namespace llama {
@@ -11,7 +13,7 @@ namespace llama {
 struct RaggedSeq {
   int q0, n_new, kv;  // first row, new tokens, keys
 };
-__device__ __forceinline__ bool ragged_seq(const RaggedAttnParams& p, int b, RaggedSeq& s, bool flag) {
+__host__ __device__ __forceinline__ bool ragged_seq(const RaggedAttnParams& p, int b, RaggedSeq& s, bool flag) {
   const int c0 = p.cu[b], c1 = p.cu[b + 1];
   s.q0 = c0;
   bool ok = c0 >= 0 && c1 >= c0 && c1 <= p.N && c1 - c0 <= p.max_new;
@@ -23,7 +25,9 @@ __device__ __forceinline__ bool ragged_seq(const RaggedAttnParams& p, int b, Rag
   }
   if (!ok) {
     s.n_new = s.kv = 0;
+#ifdef __CUDA_ARCH__
     if (flag) atomicOr(p.status, LLAMA_DEV_POS_RANGE);
+#endif
   }
   return ok;
 }
@@ -103,20 +107,26 @@ constexpr int RT_PRE = 128;  // prefix sums kept, at equal distances over the re
 constexpr int RT_UNIT = 1;
 
 // bq and KT are powers of two: no divisions (64-bit ones took most of a small call's start)
-__device__ __forceinline__ int rt_log2(int x) { return 31 - __clz(x); }
-__device__ __forceinline__ int rt_blocks(int n_new, int bq) { return (n_new + bq - 1) >> rt_log2(bq); }
+__host__ __device__ __forceinline__ int rt_log2(int x) {
+#ifdef __CUDA_ARCH__
+  return 31 - __clz(x);
+#else
+  return 31 - __builtin_clz((unsigned)x);
+#endif
+}
+__host__ __device__ __forceinline__ int rt_blocks(int n_new, int bq) { return (n_new + bq - 1) >> rt_log2(bq); }
 // q tile t of a request: its key tiles; the sum over the tiles before it (all full)
 template <int KT>
-__device__ __forceinline__ int rt_tiles(int c, int n_new, int bq, int t) {
+__host__ __device__ __forceinline__ int rt_tiles(int c, int n_new, int bq, int t) {
   const long long last = min((long long)(t + 1) * bq, (long long)n_new);
   return (int)((c + last + KT - 1) / KT);
 }
-__device__ __forceinline__ long long rt_floor_sum(long long m, int lr) {  // sum of i >> lr over i < m
+__host__ __device__ __forceinline__ long long rt_floor_sum(long long m, int lr) {  // sum of i >> lr over i < m
   const long long q = m >> lr;
   return ((q * (q - 1) / 2) << lr) + q * (m - (q << lr));
 }
 template <int KT>
-__device__ __forceinline__ long long rt_before(int c, int bq, long long t) {
+__host__ __device__ __forceinline__ long long rt_before(int c, int bq, long long t) {
   if (bq >= KT) {
     const int s = bq >> rt_log2(KT);
     return t * (((long long)c + KT - 1) / KT) + s * (t * (t + 1) / 2);
@@ -127,7 +137,7 @@ __device__ __forceinline__ long long rt_before(int c, int bq, long long t) {
   return t + rt_floor_sum(e + t, lr) - rt_floor_sum(e, lr);
 }
 template <int KT>
-__device__ __forceinline__ long long rt_total(int c, int n_new, int bq) {
+__host__ __device__ __forceinline__ long long rt_total(int c, int n_new, int bq) {
   if (n_new <= 0) return 0;
   const int nt = rt_blocks(n_new, bq);
   return rt_before<KT>(c, bq, nt - 1) + rt_tiles<KT>(c, n_new, bq, nt - 1) + (long long)RT_UNIT * nt;
@@ -148,14 +158,14 @@ struct RtWalk {
   long long xs;
 };
 
-__device__ __forceinline__ void rt_load(const RaggedAttnParams& p, int bq, RtWalk& w) {
+__host__ __device__ __forceinline__ void rt_load(const RaggedAttnParams& p, int bq, RtWalk& w) {
   ragged_seq(p, w.b, w.s, false);
   w.c = max(w.s.kv - w.s.n_new, 0);
   w.nt = rt_blocks(w.s.n_new, bq);
 }
 // to entry w.x; pre[i]: entries of one head group of the requests before i * per
 template <int KT>
-__device__ __forceinline__ void rt_start(const RaggedAttnParams& p, const long long* pre, int HG, int bq, RtWalk& w) {
+__host__ __device__ __forceinline__ void rt_start(const RaggedAttnParams& p, const long long* pre, int HG, int bq, RtWalk& w) {
   if (w.x >= w.end) return;
   int lo = 0, hi = RT_PRE - 1;  // the last i whose entries begin at or before x
   while (lo < hi) {
@@ -181,7 +191,7 @@ __device__ __forceinline__ void rt_start(const RaggedAttnParams& p, const long l
 }
 // the next segment with tiles; false at the end of the range
 template <int KT>
-__device__ __forceinline__ bool rt_segment(int bq, RtWalk& w) {
+__host__ __device__ __forceinline__ bool rt_segment(int bq, RtWalk& w) {
   while (w.x < w.end) {
     w.n = rt_tiles<KT>(w.c, w.s.n_new, bq, w.t);
     const long long take = min(RT_UNIT + w.n - w.off, w.end - w.x);
@@ -201,7 +211,7 @@ __device__ __forceinline__ bool rt_segment(int bq, RtWalk& w) {
   return false;
 }
 // on to the next unit, where the segment ended its unit
-__device__ __forceinline__ void rt_advance(const RaggedAttnParams& p, int HG, int bq, RtWalk& w) {
+__host__ __device__ __forceinline__ void rt_advance(const RaggedAttnParams& p, int HG, int bq, RtWalk& w) {
   if (w.x >= w.end) return;
   w.off = 0;
   if (++w.t < w.nt) return;
@@ -241,6 +251,66 @@ __device__ __forceinline__ void rt_prefix(const RaggedAttnParams& p, int bq, lon
   if (tid < RT_PRE) pre[tid] = x;
   if (tid == RT_PRE - 1) pre[RT_PRE] = x + sum;
   __syncthreads();
+}
+
+// Host walk of the list for lengths in host memory, with the kernels' own functions:
+// every key tile of every unit in exactly one CTA's range, in order, and each cut unit
+// merged from one partial of each CTA it spans, in the slots the merge reads, no slot or
+// counter used twice or outside the workspace. rows: query rows of a unit.
+template <int KT>
+bool check_ragged_list(const RaggedAttnParams& p, int rows, int grid) {
+  const int hpc = prefill_heads_per_cta(p.H / p.Hkv), bq = rows / hpc, HG = p.H / hpc;
+  if (rows % hpc || p.H % hpc) return false;
+  std::vector<long long> pre(RT_PRE + 1, 0);
+  const int per = (p.B + RT_PRE - 1) / RT_PRE;
+  long long units = 0;
+  for (int b = 0; b < RT_PRE * per; ++b) {
+    if (b % per == 0) pre[b / per + 1] = pre[b / per];
+    if (b >= p.B) continue;
+    RaggedSeq s;
+    ragged_seq(p, b, s, false);
+    pre[b / per + 1] += rt_total<KT>(s.kv > s.n_new ? s.kv - s.n_new : 0, s.n_new, bq);
+    units += (long long)rt_blocks(s.n_new, bq) * HG;
+  }
+  const long long W = pre[RT_PRE] * HG, G = W < grid ? W : grid;
+  std::vector<char> slot_used(2 * (size_t)grid, 0), counter_used(grid, 0);
+  long long done = 0;
+  int b = -1, zl = 0, at = 0, from = 0;  // the unit under way, its tiles so far, its first CTA
+  int t = 0;
+  for (int cta = 0; cta < G; ++cta) {
+    RtWalk w;
+    w.x = rt_begin(cta, W, G);
+    w.end = rt_begin(cta + 1, W, G);
+    const long long xbeg = w.x;
+    rt_start<KT>(p, pre.data(), HG, bq, w);
+    for (; rt_segment<KT>(bq, w); rt_advance(p, HG, bq, w)) {
+      if (w.j0 == 0) {
+        if (b >= 0) return false;  // the unit before is not done
+        b = w.b, zl = w.zl, t = w.t, at = 0, from = cta;
+      }
+      const long long c = w.s.kv > w.s.n_new ? w.s.kv - w.s.n_new : 0;
+      const long long end = (long long)(w.t + 1) * bq < w.s.n_new ? (long long)(w.t + 1) * bq : w.s.n_new;
+      if (b != w.b || zl != w.zl || t != w.t || at != w.j0 || w.n != (c + end + KT - 1) / KT || w.j1 > w.n) return false;
+      if (w.zl < 0 || w.zl >= HG || w.t * (long long)bq >= w.s.n_new) return false;
+      at = w.j1;
+      const bool whole = w.j0 == 0 && w.j1 == w.n;
+      if (!whole) {
+        const long long x0 = w.xs + RT_UNIT;
+        const int c0 = (int)rt_own(x0, W, G), c1 = (int)rt_own(x0 + w.n - 1, W, G);
+        const int slot = 2 * cta + (w.xs <= xbeg ? 0 : 1);
+        if (c0 != from || cta < c0 || cta > c1 || (w.j1 == w.n) != (cta == c1)) return false;
+        if (slot != (cta == c0 ? 2 * c0 + (w.xs <= rt_begin(c0, W, G) ? 0 : 1) : 2 * cta) || slot_used[slot]) return false;
+        slot_used[slot] = 1;
+        if (cta == c0 && counter_used[c0]) return false;
+        counter_used[c0] = 1;
+      }
+      if (w.j1 == w.n) {
+        b = -1;
+        ++done;
+      }
+    }
+  }
+  return b < 0 && done == units;
 }
 
 // packed fp32 arithmetic: two lanes of a 64-bit register per instruction

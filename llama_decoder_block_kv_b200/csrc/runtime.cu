@@ -1066,6 +1066,29 @@ int llama_selfcheck_plans(int M, int dim, int n_heads, int n_kv_heads, int ffn, 
     align_decode_sk_uniform(p1, sp + 1, num_sms);  // the grid such calls launch
     if (!check_decode_sk(p1, pos.data(), M, n_heads, n_kv_heads, D, S)) return LLAMA_ERR_INTERNAL;
   }
+  // the attention over pages and packed prompts: M requests of single tokens, chunks,
+  // whole prompts and mixtures, some without new tokens, some whose rows see no key
+  std::vector<int> cu(M + 1), kv(M);
+  for (int pattern = 0; pattern < 5; ++pattern) {
+    long long N = 0;
+    cu[0] = 0;
+    for (int b = 0; b < M; ++b) {
+      lcg = lcg * 1664525u + 1013904223u;
+      const int r = (int)((lcg >> 8) % (uint32_t)S);
+      int n = pattern == 0 ? 1
+            : pattern == 1 ? std::min(r % 300, S)
+            : pattern == 2 ? r + 1
+            : pattern == 3 ? (b % 3 == 0 ? r % 70 : b % 5 != 0)
+                           : (b == M - 1 ? S : 0);
+      if (N + n > (1LL << 30)) n = 0;
+      kv[b] = pattern == 2 || pattern == 4 ? n
+            : pattern == 3 && b % 7 == 6 ? n / 2
+                                         : std::min(S, n + (int)((lcg >> 4) % (uint32_t)S));
+      N += n;
+      cu[b + 1] = (int)N;
+    }
+    if (N > 0 && !check_ragged_plans(cu.data(), kv.data(), M, (int)N, S, n_heads, n_kv_heads, num_sms)) return LLAMA_ERR_INTERNAL;
+  }
   return LLAMA_OK;
 }
 

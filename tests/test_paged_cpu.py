@@ -119,3 +119,13 @@ def test_plain_attention_is_the_library_attention():
         q.double().transpose(0, 1), k.double().transpose(0, 1), v.double().transpose(0, 1), attn_mask=mask, enable_gqa=True)
     assert torch.allclose(out, want.transpose(0, 1), atol=1e-12)
     assert (R.attention(q, k[:2], v[:2])[0][:3] == 0).all()
+
+
+@pytest.mark.parametrize("M", [1, 2, 31, 129, 700, B.LLAMA_MAX_SEQS])
+@pytest.mark.parametrize("H,Hkv", [(4, 4), (32, 8), (64, 8), (12, 4), (20, 1)])
+def test_attention_lists_cover_every_tile_once(M, H, Hkv):
+    """The lists of key tiles of the three attention kernels, walked on the host inside llama_selfcheck_plans: single
+    tokens, chunks, whole prompts and mixtures of M requests, some without new tokens."""
+    for S in (1, 130, 8192):
+        for sms in (148, 7):
+            assert B.lib().llama_selfcheck_plans(M, H * 64, H, Hkv, 1024, S, sms) == B.LLAMA_OK, (M, H, Hkv, S, sms)
