@@ -73,6 +73,7 @@ namespace {
 constexpr int RT_KT = 128;  // keys per tile (a K or V stage)
 constexpr int RT_THREADS = 384;
 constexpr int RT_SEGS = 3;  // segments queued ahead
+constexpr int RT_FEW = 64;       // rows up to which all threads merge a cut unit, not a thread per row
 constexpr int RT_LEADER = 128;  // first softmax thread
 constexpr float RT_LOG2E = 1.4426950408889634f;
 constexpr float RT_RESCALE = 8.0f;  // raise the running maximum only past 2^8
@@ -469,6 +470,11 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     const int pos_l = r / hpc, hl = r - pos_l * hpc;
     const int stride = 256 * D + 512;  // floats of one partial
     uint8_t* out = sOut + (warp - 4) * Cfg::OUT;
+    // the prefix sums have been read by the time a segment is out: (maximum, 1 / sum) of a
+    // merged unit's rows, and a bit for each row that is not finite
+    float2* few = reinterpret_cast<float2*>(pre);
+    unsigned* few_bad = reinterpret_cast<unsigned*>(few + RT_FEW);
+    static_assert(RT_FEW * 8 + 8 <= RT_PRE * 8 && RT_FEW <= 64, "room in the prefix sums");
     const int tok_end = 31 / hpc + quarter * 32 / hpc;  // the warp's last token, in the tile
     int sc = 0, oc = 0;                // S tiles taken, segments with work
     int n = 0;                         // key tiles walked (ring slots 2 n, 2 n + 1)
@@ -607,6 +613,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
       const bool store = tok < w.s.n_new && lim > 0;
       bf16* dst = reinterpret_cast<bf16*>(p.o) + ((size_t)(w.s.q0 + tok) * p.H + h) * D;
       bool bad = false;  // the row's result is not finite
+      const int rows = (int)min((long long)(w.s.n_new - w.tok0) * hpc, 256LL);  // rows of the request in the unit
       if (w.whole) {
         const float inv = last < 0 ? 0.f : 1.f / l;  // a row without keys is zero
         // 32 rows of the request leave as boxes of 64 columns, by way of shared memory:
@@ -694,9 +701,9 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
           // partials of CTAs c0 .. c1 in that order; c0 holds the unit in its second slot
           // unless its range starts inside it, the others in their first
           const int slot0 = w.slot0;
+          // batches of independent loads: one by one they would cost an L2 round trip each
+          auto slot = [&](int c) { return part + (size_t)(c == c0 ? slot0 : 2 * c) * stride; };
           if (store) {
-            // batches of independent loads: one by one they would cost an L2 round trip each
-            auto slot = [&](int c) { return part + (size_t)(c == c0 ? slot0 : 2 * c) * stride; };
             float mm = -INFINITY, ll = 0.f;
             for (int c = c0; c <= c1; c += 16) {
               float2 v[16];
@@ -715,8 +722,9 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
             }
             const float inv = last < 0 ? 0.f : 1.f / ll;
             merged = ll;
+            if (rows <= RT_FEW) few[row] = make_float2(mm, last < 0 ? -1.f : inv);  // -1: a row without keys
 #pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
+            for (int d = 0; rows > RT_FEW && d < D; d += 32) {
               float acc[32];
 #pragma unroll
               for (int e = 0; e < 32; ++e) acc[e] = 0.f;
@@ -754,10 +762,55 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
             }
           }
           bad = bad && merged > 0.f;
+          if (rows <= RT_FEW) {
+            // few rows (single tokens, short chunks over long histories): 4 columns of a row at
+            // a time, over all threads; with a thread per row the merge of 18 partials of 16
+            // rows took most of 42 us
+            if (tid == RT_LEADER) few_bad[0] = few_bad[1] = 0;
+            meet_all();
+            if (!ok) break;
+            for (int it = tid - RT_LEADER; it < rows * (D / 4); it += 256) {
+              const int c4 = it / rows, rr = it - c4 * rows;
+              const float2 mi = few[rr];
+              float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int c = c0; c <= c1; c += 8) {
+                float m_c[8];
+                float4 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float* pc = slot(min(c + k, c1));
+                  m_c[k] = c + k <= c1 ? __ldcg(reinterpret_cast<const float2*>(pc + 256 * D) + rr).x : -INFINITY;
+                  v[k] = __ldcg(reinterpret_cast<const float4*>(pc) + c4 * 256 + rr);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  if (m_c[k] == -INFINITY) continue;  // no weight there (and perhaps no O)
+                  const float f = rt_ex2(m_c[k] - mi.x);
+                  acc.x += v[k].x * f;
+                  acc.y += v[k].y * f;
+                  acc.z += v[k].z * f;
+                  acc.w += v[k].w * f;
+                }
+              }
+              float y[4] = {acc.x * mi.y, acc.y * mi.y, acc.z * mi.y, acc.w * mi.y};
+              bool odd = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (mi.y == -1.f) y[e] = 0.f;
+                odd |= !(fabsf(y[e]) < INFINITY);
+              }
+              if (odd && mi.y < INFINITY) atomicOr(&few_bad[rr >> 5], 1u << (rr & 31));
+              store4(reinterpret_cast<bf16*>(p.o) +
+                         ((size_t)(w.s.q0 + w.tok0 + rr / hpc) * p.H + w.h0 + rr % hpc) * D + 4 * c4,
+                     y);
+            }
+          }
           if (tid == RT_LEADER) counters[c0] = 0;  // re-armed for the next launch
         }
+        const bool merger = *s_last;
         meet_all();  // s_last is written again by the next cut segment
         if (!ok) break;
+        if (merger && rows <= RT_FEW && g == 0 && r < rows) bad = (few_bad[r >> 5] >> (r & 31)) & 1;
       }
       for (unsigned todo = __ballot_sync(0xffffffffu, bad); todo; todo &= todo - 1) {
         const int src = __ffs(todo) - 1;
