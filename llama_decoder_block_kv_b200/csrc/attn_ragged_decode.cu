@@ -604,8 +604,11 @@ bool check_ragged_plans(const int* cu, const int* kv_lens, int B, int N, int max
   p.Hkv = Hkv;
   p.page_shift = 4;
   p.max_pages = (max_kv + 15) / 16;
-  bool ok = check_ragged_list<128>(p, 256, std::min(num_sms, RAGGED_TC_CTAS));
-  for (int per_sm : {4, 2}) ok = ok && check_ragged_list<64>(p, 32, std::min(num_sms, RAGGED_F32_CTAS / 4) * per_sm);
+  bool ok = true;
+  for (bool units : {false, true}) {
+    ok = ok && check_ragged_list<128>(p, 256, std::min(num_sms, RAGGED_TC_CTAS), units);
+    for (int per_sm : {3, 2}) ok = ok && check_ragged_list<64>(p, 32, std::min(num_sms, RAGGED_F32_CTAS / 3) * per_sm, units);
+  }
   p.max_new = 1;  // requests with more are skipped there
   return ok && check_decode_list(p, std::min(2 * num_sms, RAGGED_DECODE_CTAS));
 }

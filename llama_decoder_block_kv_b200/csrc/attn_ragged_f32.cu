@@ -14,10 +14,10 @@
 // shared memory serves 8 products. K(j + 1) is copied while P(j) V(j) runs and V(j + 1)
 // while the scores of j + 1 are taken (cp.async; keys past the last one are zeros).
 //
-// Measured at 4/2 heads of 64: 7 prompts of 5..509 tokens 28.9 us, 5 requests of up to
-// 761 keys with up to 61 new tokens 17.9 us; of a CTA's 15 us there 5 pass before it
-// knows its range and 3 until its first tile is in, the rest is one or two tiles and the
-// merge of the cut unit.
+// Measured at 4/2 heads of 64: 7 prompts of 5..509 tokens 23.6 us (four CTAs per SM, which
+// spill: 32 us), 5 requests of up to 761 keys with up to 61 new tokens 17.5 us; of a CTA's
+// time there 3 us pass before it knows its range and 3 until its first tile is in, the rest
+// is one or two tiles and the merge of the cut unit.
 //
 // A V row of a later key that is not finite reaches the earlier rows of its tile (0 x
 // NaN): rows whose result is not finite are computed again, key by key (unless their sum
@@ -32,6 +32,7 @@ namespace {
 constexpr int RF_KT = 64;       // keys per tile
 constexpr int RF_ROWS = 32;     // query rows per unit
 constexpr int RF_THREADS = 128;
+constexpr int RF_MERGE = 3;     // what the merge of a cut unit costs, in tiles
 constexpr float RF_LOG2E = 1.4426950408889634f;
 }  // namespace
 
@@ -41,7 +42,7 @@ struct RfCfg {
   static constexpr int LDP = RF_KT + 4;
   static constexpr int FLOATS = RF_ROWS * LD + RF_KT * LD + RF_KT * D + RF_ROWS * LDP;
   static constexpr size_t SMEM = FLOATS * 4;
-  static constexpr int PER_SM = D == 64 ? 4 : 2;  // resident CTAs (shared memory)
+  static constexpr int PER_SM = D == 64 ? 3 : 2;  // resident CTAs (a fourth fits in shared memory, but spills registers)
 };
 
 __device__ __forceinline__ void rf_copy16(void* dst, const void* src, int bytes) {  // bytes 0: zeros
@@ -71,16 +72,16 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
   float* sV = sK + RF_KT * LD;
   float* sP = sV + RF_KT * D;
   __shared__ long long pre[RT_PRE + 1];
-  __shared__ long long s_w[RF_THREADS / 32];
+  __shared__ long long s_w[3 * RF_THREADS / 32];
   __shared__ int s_last;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tx = tid & 15, ty = tid >> 4;
   const int n_rep = p.H / p.Hkv, groups = n_rep / hpc, HG = p.Hkv * groups, bq = RF_ROWS / hpc;
   const int stride = RF_ROWS * D + 2 * RF_ROWS;  // floats of one partial
   const float sl2 = rsqrtf((float)D) * RF_LOG2E;
-  rt_prefix<RF_KT>(p, bq, pre, s_w);
-  const long long W = pre[RT_PRE] * HG, G = min((long long)gridDim.x, W), cta = blockIdx.x;
   RtWalk w;
+  w.units = rt_prefix<RF_KT, RF_MERGE>(p, bq, HG, pre, s_w);
+  const long long W = pre[RT_PRE] * HG, G = min((long long)gridDim.x, W), cta = blockIdx.x;
   w.x = cta < G ? rt_begin(cta, W, G) : 0;
   w.end = cta < G ? rt_begin(cta + 1, W, G) : 0;
   const long long xbeg = w.x;
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
 // ------------------------------------------------------------------ host side
 
 size_t ragged_f32_ws_floats(int D) {
-  return (size_t)2 * (D == 64 ? RAGGED_F32_CTAS : RAGGED_F32_CTAS / 2) * (RF_ROWS * D + 2 * RF_ROWS);
+  return (size_t)2 * (RAGGED_F32_CTAS / 3 * (D == 64 ? 3 : 2)) * (RF_ROWS * D + 2 * RF_ROWS);
 }
 
 template <int D>
@@ -356,7 +357,7 @@ static cudaError_t ragged_f32(const RaggedAttnParams& p, float* part, int* count
   static std::atomic<unsigned long long> attr{0};
   cudaError_t e = ensure_smem(attn_ragged_f32_kernel<D>, RfCfg<D>::SMEM, attr);
   if (e != cudaSuccess) return e;
-  const int grid = std::min(num_sms, RAGGED_F32_CTAS / 4) * RfCfg<D>::PER_SM;
+  const int grid = std::min(num_sms, RAGGED_F32_CTAS / 3) * RfCfg<D>::PER_SM;
   attn_ragged_f32_kernel<D><<<grid, RF_THREADS, RfCfg<D>::SMEM, st>>>(p, part, counters,
                                                                       prefill_heads_per_cta(p.H / p.Hkv));
   return cudaGetLastError();

@@ -73,6 +73,7 @@ namespace {
 constexpr int RT_KT = 128;  // keys per tile (a K or V stage)
 constexpr int RT_THREADS = 384;
 constexpr int RT_SEGS = 3;  // segments queued ahead
+constexpr int RT_MERGE = 6;      // what the merge of a cut unit costs, in tiles
 constexpr int RT_FEW = 64;       // rows up to which all threads merge a cut unit, not a thread per row
 constexpr int RT_LEADER = 128;  // first softmax thread
 constexpr float RT_LOG2E = 1.4426950408889634f;
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
   RtSeg* segs = reinterpret_cast<RtSeg*>(tmem_slot + 4);
   // entries of one head group of the requests before i * per, per = ceil(B / RT_PRE)
   long long* pre = reinterpret_cast<long long*>((reinterpret_cast<uintptr_t>(segs + RT_SEGS) + 7) & ~uintptr_t(7));  // [RT_PRE + 1]
-  __shared__ long long s_w[RT_THREADS / 32];
+  __shared__ long long s_w[3 * RT_THREADS / 32];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_rep = p.H / p.Hkv, groups = n_rep / hpc, HG = p.Hkv * groups;
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  rt_prefix<RT_KT>(p, bq, pre, s_w);
+  const bool units = rt_prefix<RT_KT, RT_MERGE>(p, bq, HG, pre, s_w);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // segment k, or false at the end of the range (or after a timeout); given back by leave()
@@ -426,6 +427,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
       // ------------------------------------------------------------------ scheduler
       const long long W = pre[RT_PRE] * HG, G = min((long long)gridDim.x, W), cta = blockIdx.x;
       RtWalk w;
+      w.units = units;
       w.x = cta < G ? rt_begin(cta, W, G) : 0;
       w.end = cta < G ? rt_begin(cta + 1, W, G) : 0;
       const long long xbeg = w.x;

@@ -226,7 +226,7 @@ size_t ragged_ws_bytes(int dtype, int D);
 int ragged_attention(const RaggedAttnParams& p, int dtype, void* workspace, cudaStream_t st);
 
 // attn_ragged_f32.cu: partials and counters of RAGGED_F32_CTAS CTAs
-constexpr int RAGGED_F32_CTAS = 592;  // at most this many CTAs: four per SM (head_dim 64), or two
+constexpr int RAGGED_F32_CTAS = 444;  // at most this many CTAs: three per SM (head_dim 64), or two
 size_t ragged_f32_ws_floats(int D);
 cudaError_t launch_attn_ragged_f32(const RaggedAttnParams& p, float* part, int* counters, int num_sms, cudaStream_t st);
 // attn_ragged_tc.cu (bf16): partials of RAGGED_TC_CTAS CTAs and one counter each, zeroed once

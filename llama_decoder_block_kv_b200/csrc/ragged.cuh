@@ -102,7 +102,8 @@ __device__ void ragged_row(const RaggedAttnParams& p, int b, const RaggedSeq& s,
 // consecutive new tokens x hpc heads; it needs the key tiles (KT keys each) up to its
 // last position. The units, request by request, kv head by kv head, stand in one list
 // that is cut into equal contiguous ranges, one per CTA. A unit takes RT_UNIT entries
-// of it for what it costs besides its tiles, and one per tile.
+// of it for what it costs besides its tiles, and one per tile. Where cutting units would
+// gain less than their merge costs, every unit takes one entry and none is cut (w.units).
 constexpr int RT_PRE = 128;  // prefix sums kept, at equal distances over the requests
 constexpr int RT_UNIT = 1;
 
@@ -137,10 +138,16 @@ __host__ __device__ __forceinline__ long long rt_before(int c, int bq, long long
   return t + rt_floor_sum(e + t, lr) - rt_floor_sum(e, lr);
 }
 template <int KT>
-__host__ __device__ __forceinline__ long long rt_total(int c, int n_new, int bq) {
+__host__ __device__ __forceinline__ long long rt_total(int c, int n_new, int bq, bool units) {
   if (n_new <= 0) return 0;
   const int nt = rt_blocks(n_new, bq);
+  if (units) return nt;
   return rt_before<KT>(c, bq, nt - 1) + rt_tiles<KT>(c, n_new, bq, nt - 1) + (long long)RT_UNIT * nt;
+}
+// entries of a request before its q tile t
+template <int KT>
+__host__ __device__ __forceinline__ long long rt_entry(int c, int bq, int t, bool units) {
+  return units ? t : rt_before<KT>(c, bq, t) + (long long)RT_UNIT * t;
 }
 __host__ __device__ __forceinline__ long long rt_begin(long long c, long long W, long long G) { return c * W / G; }
 __host__ __device__ __forceinline__ long long rt_own(long long x, long long W, long long G) { return ((x + 1) * G - 1) / W; }
@@ -148,6 +155,7 @@ __host__ __device__ __forceinline__ long long rt_own(long long x, long long W, l
 // A CTA's walk over its range [x, end) of the list.
 struct RtWalk {
   long long x, end;
+  bool units;    // the list's entries are units
   int b, zl, t;  // request, (kv head, head group), q tile
   RaggedSeq s;
   int c, nt;       // keys before the new tokens, q tiles
@@ -175,7 +183,7 @@ __host__ __device__ __forceinline__ void rt_start(const RaggedAttnParams& p, con
   long long off = w.x - pre[lo] * HG, per = 0;
   for (w.b = lo * ((p.B + RT_PRE - 1) / RT_PRE);; ++w.b) {
     rt_load(p, bq, w);
-    per = rt_total<KT>(w.c, w.s.n_new, bq);
+    per = rt_total<KT>(w.c, w.s.n_new, bq, w.units);
     if (off < per * HG || w.b == p.B - 1) break;
     off -= per * HG;
   }
@@ -184,20 +192,20 @@ __host__ __device__ __forceinline__ void rt_start(const RaggedAttnParams& p, con
   int a = 0, z = w.nt - 1;
   while (a < z) {
     const int mid = (a + z + 1) >> 1;
-    if (rt_before<KT>(w.c, bq, mid) + (long long)RT_UNIT * mid <= off) a = mid; else z = mid - 1;
+    if (rt_entry<KT>(w.c, bq, mid, w.units) <= off) a = mid; else z = mid - 1;
   }
   w.t = a;
-  w.off = off - rt_before<KT>(w.c, bq, a) - (long long)RT_UNIT * a;
+  w.off = off - rt_entry<KT>(w.c, bq, a, w.units);
 }
 // the next segment with tiles; false at the end of the range
 template <int KT>
 __host__ __device__ __forceinline__ bool rt_segment(int bq, RtWalk& w) {
   while (w.x < w.end) {
     w.n = rt_tiles<KT>(w.c, w.s.n_new, bq, w.t);
-    const long long take = min(RT_UNIT + w.n - w.off, w.end - w.x);
+    const long long take = w.units ? 1 : min(RT_UNIT + w.n - w.off, w.end - w.x);
     w.xs = w.x - w.off;
-    w.j0 = (int)max(w.off - RT_UNIT, 0LL);
-    w.j1 = (int)max(w.off + take - RT_UNIT, 0LL);
+    w.j0 = w.units ? 0 : (int)max(w.off - RT_UNIT, 0LL);
+    w.j1 = w.units ? w.n : (int)max(w.off + take - RT_UNIT, 0LL);
     w.x += take;
     w.off += take;
     if (w.j1 > w.j0) {
@@ -226,31 +234,57 @@ __host__ __device__ __forceinline__ void rt_advance(const RaggedAttnParams& p, i
 
 // Prefix sums of the requests' list entries (one head group), by all threads of a CTA
 // (at least RT_PRE); pre[i]: those of the requests before i * ceil(B / RT_PRE).
-// Ends with a barrier; s_w: a value per warp.
-template <int KT>
-__device__ __forceinline__ void rt_prefix(const RaggedAttnParams& p, int bq, long long* pre, long long* s_w) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+// Returns whether the entries are units: where the CTA with the most of them takes no
+// more tiles than an equal share and MERGE, the merge's cost in tiles. Ends with a
+// barrier; s_w: three values per warp.
+template <int KT, int MERGE>
+__device__ __forceinline__ bool rt_prefix(const RaggedAttnParams& p, int bq, int HG, long long* pre, long long* s_w) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
   const int per = (p.B + RT_PRE - 1) / RT_PRE;  // the first RT_PRE threads take them
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  long long sum = 0;
+  long long sum[2] = {0, 0}, most = 0;  // entries by tiles and by units, entries of the longest unit
   RaggedSeq s;
   for (int b = b0; b < b1; ++b) {
     ragged_seq(p, b, s, blockIdx.x == 0);
-    sum += rt_total<KT>(max(s.kv - s.n_new, 0), s.n_new, bq);
+    if (s.n_new == 0) continue;
+    const int c = max(s.kv - s.n_new, 0), nt = rt_blocks(s.n_new, bq);
+    sum[0] += rt_total<KT>(c, s.n_new, bq, false);
+    sum[1] += nt;
+    most = max(most, (long long)RT_UNIT + rt_tiles<KT>(c, s.n_new, bq, nt - 1));
   }
-  long long x = sum;
+  long long x[2] = {sum[0], sum[1]};
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const long long y = __shfl_up_sync(0xffffffffu, x[i], o);
+      if (lane >= o) x[i] += y;
+    }
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
   }
-  if (lane == 31) s_w[warp] = x;
+  if (lane == 31) {
+    s_w[warp] = x[0];
+    s_w[warps + warp] = x[1];
+    s_w[2 * warps + warp] = most;
+  }
   __syncthreads();
-  x -= sum;
-  for (int w = 0; w < warp; ++w) x += s_w[w];
-  if (tid < RT_PRE) pre[tid] = x;
-  if (tid == RT_PRE - 1) pre[RT_PRE] = x + sum;
+  long long total[2] = {0, 0};
+  x[0] -= sum[0];
+  x[1] -= sum[1];
+  for (int w = 0; w < warps; ++w) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (w < warp) x[i] += s_w[i * warps + w];
+      total[i] += s_w[i * warps + w];
+    }
+    most = max(most, s_w[2 * warps + w]);
+  }
+  const long long G = gridDim.x, U = total[1] * HG;
+  const bool units = U < (1LL << 30) && (long long)((unsigned)(U + G - 1) / (unsigned)G) * most * G <= total[0] * HG + MERGE * G;
+  if (tid < RT_PRE) pre[tid] = units ? x[1] : x[0];
+  if (tid == RT_PRE - 1) pre[RT_PRE] = units ? total[1] : total[0];
   __syncthreads();
+  return units;
 }
 
 // Host walk of the list for lengths in host memory, with the kernels' own functions:
@@ -258,7 +292,7 @@ __device__ __forceinline__ void rt_prefix(const RaggedAttnParams& p, int bq, lon
 // merged from one partial of each CTA it spans, in the slots the merge reads, no slot or
 // counter used twice or outside the workspace. rows: query rows of a unit.
 template <int KT>
-bool check_ragged_list(const RaggedAttnParams& p, int rows, int grid) {
+bool check_ragged_list(const RaggedAttnParams& p, int rows, int grid, bool by_units) {
   const int hpc = prefill_heads_per_cta(p.H / p.Hkv), bq = rows / hpc, HG = p.H / hpc;
   if (rows % hpc || p.H % hpc) return false;
   std::vector<long long> pre(RT_PRE + 1, 0);
@@ -269,7 +303,7 @@ bool check_ragged_list(const RaggedAttnParams& p, int rows, int grid) {
     if (b >= p.B) continue;
     RaggedSeq s;
     ragged_seq(p, b, s, false);
-    pre[b / per + 1] += rt_total<KT>(s.kv > s.n_new ? s.kv - s.n_new : 0, s.n_new, bq);
+    pre[b / per + 1] += rt_total<KT>(s.kv > s.n_new ? s.kv - s.n_new : 0, s.n_new, bq, by_units);
     units += (long long)rt_blocks(s.n_new, bq) * HG;
   }
   const long long W = pre[RT_PRE] * HG, G = W < grid ? W : grid;
@@ -279,6 +313,7 @@ bool check_ragged_list(const RaggedAttnParams& p, int rows, int grid) {
   int t = 0;
   for (int cta = 0; cta < G; ++cta) {
     RtWalk w;
+    w.units = by_units;
     w.x = rt_begin(cta, W, G);
     w.end = rt_begin(cta + 1, W, G);
     const long long xbeg = w.x;
@@ -294,6 +329,7 @@ bool check_ragged_list(const RaggedAttnParams& p, int rows, int grid) {
       if (w.zl < 0 || w.zl >= HG || w.t * (long long)bq >= w.s.n_new) return false;
       at = w.j1;
       const bool whole = w.j0 == 0 && w.j1 == w.n;
+      if (by_units && !whole) return false;
       if (!whole) {
         const long long x0 = w.xs + RT_UNIT;
         const int c0 = (int)rt_own(x0, W, G), c1 = (int)rt_own(x0 + w.n - 1, W, G);
