@@ -46,9 +46,6 @@ __device__ __forceinline__ float rd_quad_sum(float v) {
   return v + __shfl_xor_sync(0xffffffffu, v, 2);
 }
 
-__host__ __device__ __forceinline__ long long rd_begin(long long c, long long W, long long G) { return c * W / G; }
-__host__ __device__ __forceinline__ long long rd_own(long long x, long long W, long long G) { return ((x + 1) * G - 1) / W; }
-
 // tiles of one unit of a request with kv keys (one for a token that sees none: its
 // row is written as zeros), 0 for a request without a new token (kv = -1)
 __host__ __device__ __forceinline__ int rd_tiles(int kv) { return kv < 0 ? 0 : kv == 0 ? 1 : (kv - 1) / RD_KT + 1; }
@@ -68,7 +65,7 @@ __host__ __device__ __forceinline__ RdUnit rd_locate(const long long* pb, const 
   u.b = lo;
   const long long off = x - pb[lo] * HG;
   const int n = rd_tiles(kvs[lo]);
-  u.zl = (int)(off / n);
+  u.zl = (int)rt_div(off, n);
   u.t = (int)(off - (long long)u.zl * n);
   return u;
 }
@@ -157,7 +154,7 @@ __global__ void __launch_bounds__(160, 2)
     __syncthreads();
   }
   const long long W = pb[B] * HG, G = min((long long)gridDim.x, W), cta = blockIdx.x;
-  const long long sbeg = cta < G ? rd_begin(cta, W, G) : 0, send = cta < G ? rd_begin(cta + 1, W, G) : 0;
+  const long long sbeg = cta < G ? rt_begin(cta, W, G) : 0, send = cta < G ? rt_begin(cta + 1, W, G) : 0;
 
   if (warp == 4) {
     // ---------------------------------------------------------------- producer
@@ -485,7 +482,7 @@ __global__ void __launch_bounds__(160, 2)
     if (lane == 0) mbar_arrive(&empty[st]);
 
     if (!whole) {
-      const int c0 = (int)rd_own(P, W, G), c1 = (int)rd_own(P + n_u - 1, W, G);
+      const int c0 = (int)rt_own(P, W, G), c1 = (int)rt_own(P + n_u - 1, W, G);
       // a CTA begins at most one unit that runs past its range: its counter serves it
       if (tid == 0) s_last = (atomic_add_acq_rel(&counters[c0], 1) == c1 - c0);
       asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -494,7 +491,7 @@ __global__ void __launch_bounds__(160, 2)
         // order: m = max m_c, l = sum l_c 2^(m_c - m), o = sum o_c 2^(m_c - m) / l.
         // CTA c0 holds the unit in its second slot unless its range starts at
         // the unit; every later contributor holds it in its first slot.
-        const int slot0 = 2 * c0 + (rd_begin(c0, W, G) == P ? 0 : 1);
+        const int slot0 = 2 * c0 + (rt_begin(c0, W, G) == P ? 0 : 1);
         for (int e = tid; e < hpc * D / 4; e += 128) {
           const int r = (4 * e) / D, d = 4 * e - r * D;
           // batches of independent loads: one by one they would cost an L2 round trip each
@@ -567,7 +564,7 @@ static bool check_decode_list(const RaggedAttnParams& p, int grid) {
   std::vector<char> slot_used(2 * (size_t)grid, 0), counter_used(grid, 0);
   long long done = 0, next = 0;
   for (int cta = 0; cta < G; ++cta) {
-    const long long sbeg = rd_begin(cta, W, G), send = rd_begin(cta + 1, W, G);
+    const long long sbeg = rt_begin(cta, W, G), send = rt_begin(cta + 1, W, G);
     if (sbeg != next) return false;
     next = send;
     for (long long x = sbeg; x < send;) {
@@ -576,9 +573,9 @@ static bool check_decode_list(const RaggedAttnParams& p, int grid) {
       if (n < 1 || u.zl < 0 || u.zl >= HG || u.t < 0 || u.t >= n || pb[u.b] * HG + (long long)u.zl * n + u.t != x) return false;
       const long long len = n - u.t < send - x ? n - u.t : send - x, P = x - u.t;
       if (u.t > 0 || len < n) {
-        const int c0 = (int)rd_own(P, W, G), c1 = (int)rd_own(P + n - 1, W, G), slot = 2 * cta + (P <= sbeg ? 0 : 1);
+        const int c0 = (int)rt_own(P, W, G), c1 = (int)rt_own(P + n - 1, W, G), slot = 2 * cta + (P <= sbeg ? 0 : 1);
         if (cta < c0 || cta > c1 || (u.t == 0) != (cta == c0) || (u.t + len == n) != (cta == c1)) return false;
-        if (slot != (cta == c0 ? 2 * c0 + (rd_begin(c0, W, G) == P ? 0 : 1) : 2 * cta) || slot_used[slot]) return false;
+        if (slot != (cta == c0 ? 2 * c0 + (rt_begin(c0, W, G) == P ? 0 : 1) : 2 * cta) || slot_used[slot]) return false;
         slot_used[slot] = 1;
         if (cta == c0 && counter_used[c0]) return false;
         counter_used[c0] = 1;

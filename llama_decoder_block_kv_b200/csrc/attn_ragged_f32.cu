@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
   float* sV = sK + RF_KT * LD;
   float* sP = sV + RF_KT * D;
   __shared__ long long pre[RT_PRE + 1];
-  __shared__ long long s_w[3 * RF_THREADS / 32];
+  __shared__ long long s_w[3 * RT_PRE / 32];
   __shared__ int s_last;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tx = tid & 15, ty = tid >> 4;

@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
   RtSeg* segs = reinterpret_cast<RtSeg*>(tmem_slot + 4);
   // entries of one head group of the requests before i * per, per = ceil(B / RT_PRE)
   long long* pre = reinterpret_cast<long long*>((reinterpret_cast<uintptr_t>(segs + RT_SEGS) + 7) & ~uintptr_t(7));  // [RT_PRE + 1]
-  __shared__ long long s_w[3 * RT_THREADS / 32];
+  __shared__ long long s_w[3 * RT_PRE / 32];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_rep = p.H / p.Hkv, groups = n_rep / hpc, HG = p.Hkv * groups;

@@ -14,13 +14,13 @@ struct RaggedSeq {
   int q0, n_new, kv;  // first row, new tokens, keys
 };
 __host__ __device__ __forceinline__ bool ragged_seq(const RaggedAttnParams& p, int b, RaggedSeq& s, bool flag) {
-  const int c0 = p.cu[b], c1 = p.cu[b + 1];
+  const int c0 = p.cu[b], c1 = p.cu[b + 1], kv = p.tables ? p.kv_lens[b] : 0;
   s.q0 = c0;
   bool ok = c0 >= 0 && c1 >= c0 && c1 <= p.N && c1 - c0 <= p.max_new;
   s.n_new = ok ? c1 - c0 : 0;
   s.kv = ok ? s.n_new : 0;
   if (p.tables && ok) {
-    s.kv = p.kv_lens[b];
+    s.kv = kv;
     ok = s.kv >= 0 && s.kv <= (p.max_pages << p.page_shift);
   }
   if (!ok) {
@@ -149,8 +149,15 @@ template <int KT>
 __host__ __device__ __forceinline__ long long rt_entry(int c, int bq, int t, bool units) {
   return units ? t : rt_before<KT>(c, bq, t) + (long long)RT_UNIT * t;
 }
-__host__ __device__ __forceinline__ long long rt_begin(long long c, long long W, long long G) { return c * W / G; }
-__host__ __device__ __forceinline__ long long rt_own(long long x, long long W, long long G) { return ((x + 1) * G - 1) / W; }
+// a / b of numbers that are not negative, in 32 bits where they fit (a 64-bit division is
+// some hundreds of cycles, and a call starts with several)
+__host__ __device__ __forceinline__ long long rt_div(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+__host__ __device__ __forceinline__ long long rt_begin(long long c, long long W, long long G) { return rt_div(c * W, G); }
+__host__ __device__ __forceinline__ long long rt_own(long long x, long long W, long long G) {
+  return rt_div((x + 1) * G - 1, W);
+}
 
 // A CTA's walk over its range [x, end) of the list.
 struct RtWalk {
@@ -187,7 +194,7 @@ __host__ __device__ __forceinline__ void rt_start(const RaggedAttnParams& p, con
     if (off < per * HG || w.b == p.B - 1) break;
     off -= per * HG;
   }
-  w.zl = off < (1LL << 31) && per < (1LL << 31) ? (int)((unsigned)off / (unsigned)per) : (int)(off / per);
+  w.zl = (int)rt_div(off, per);
   off -= w.zl * per;
   int a = 0, z = w.nt - 1;
   while (a < z) {
@@ -236,11 +243,12 @@ __host__ __device__ __forceinline__ void rt_advance(const RaggedAttnParams& p, i
 // (at least RT_PRE); pre[i]: those of the requests before i * ceil(B / RT_PRE).
 // Returns whether the entries are units: where the CTA with the most of them takes no
 // more tiles than an equal share and MERGE, the merge's cost in tiles. Ends with a
-// barrier; s_w: three values per warp.
+// barrier; s_w: three values per warp of the first RT_PRE threads.
 template <int KT, int MERGE>
 __device__ __forceinline__ bool rt_prefix(const RaggedAttnParams& p, int bq, int HG, long long* pre, long long* s_w) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
-  const int per = (p.B + RT_PRE - 1) / RT_PRE;  // the first RT_PRE threads take them
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int warps = RT_PRE / 32;  // the first RT_PRE threads take them
+  const int per = (p.B + RT_PRE - 1) / RT_PRE;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   long long sum[2] = {0, 0}, most = 0;  // entries by tiles and by units, entries of the longest unit
   RaggedSeq s;
@@ -262,7 +270,7 @@ __device__ __forceinline__ bool rt_prefix(const RaggedAttnParams& p, int bq, int
     }
     most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
   }
-  if (lane == 31) {
+  if (lane == 31 && warp < warps) {
     s_w[warp] = x[0];
     s_w[warps + warp] = x[1];
     s_w[2 * warps + warp] = most;
@@ -271,6 +279,7 @@ __device__ __forceinline__ bool rt_prefix(const RaggedAttnParams& p, int bq, int
   long long total[2] = {0, 0};
   x[0] -= sum[0];
   x[1] -= sum[1];
+#pragma unroll
   for (int w = 0; w < warps; ++w) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
