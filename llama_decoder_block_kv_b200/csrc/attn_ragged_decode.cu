@@ -65,7 +65,7 @@ __host__ __device__ __forceinline__ RdUnit rd_locate(const long long* pb, const 
   u.b = lo;
   const long long off = x - pb[lo] * HG;
   const int n = rd_tiles(kvs[lo]);
-  u.zl = (int)rt_div(off, n);
+  u.zl = (int)(off / n);
   u.t = (int)(off - (long long)u.zl * n);
   return u;
 }

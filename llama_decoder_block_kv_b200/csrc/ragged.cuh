@@ -14,13 +14,13 @@ struct RaggedSeq {
   int q0, n_new, kv;  // first row, new tokens, keys
 };
 __host__ __device__ __forceinline__ bool ragged_seq(const RaggedAttnParams& p, int b, RaggedSeq& s, bool flag) {
-  const int c0 = p.cu[b], c1 = p.cu[b + 1], kv = p.tables ? p.kv_lens[b] : 0;
+  const int c0 = p.cu[b], c1 = p.cu[b + 1];
   s.q0 = c0;
   bool ok = c0 >= 0 && c1 >= c0 && c1 <= p.N && c1 - c0 <= p.max_new;
   s.n_new = ok ? c1 - c0 : 0;
   s.kv = ok ? s.n_new : 0;
   if (p.tables && ok) {
-    s.kv = kv;
+    s.kv = p.kv_lens[b];
     ok = s.kv >= 0 && s.kv <= (p.max_pages << p.page_shift);
   }
   if (!ok) {
@@ -149,14 +149,9 @@ template <int KT>
 __host__ __device__ __forceinline__ long long rt_entry(int c, int bq, int t, bool units) {
   return units ? t : rt_before<KT>(c, bq, t) + (long long)RT_UNIT * t;
 }
-// a / b of numbers that are not negative, in 32 bits where they fit (a 64-bit division is
-// some hundreds of cycles, and a call starts with several)
-__host__ __device__ __forceinline__ long long rt_div(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
-}
-__host__ __device__ __forceinline__ long long rt_begin(long long c, long long W, long long G) { return rt_div(c * W, G); }
+__host__ __device__ __forceinline__ long long rt_begin(long long c, long long W, long long G) { return c * W / G; }
 __host__ __device__ __forceinline__ long long rt_own(long long x, long long W, long long G) {
-  return rt_div((x + 1) * G - 1, W);
+  return ((x + 1) * G - 1) / W;
 }
 
 // A CTA's walk over its range [x, end) of the list.
@@ -194,7 +189,7 @@ __host__ __device__ __forceinline__ void rt_start(const RaggedAttnParams& p, con
     if (off < per * HG || w.b == p.B - 1) break;
     off -= per * HG;
   }
-  w.zl = (int)rt_div(off, per);
+  w.zl = off < (1LL << 31) && per < (1LL << 31) ? (int)((unsigned)off / (unsigned)per) : (int)(off / per);
   off -= w.zl * per;
   int a = 0, z = w.nt - 1;
   while (a < z) {
