@@ -32,7 +32,6 @@ __host__ __device__ __forceinline__ bool ragged_seq(const RaggedAttnParams& p, i
   return ok;
 }
 
-
 // Row tok of the request, query head h, by one warp: softmax(q.k / sqrt(D)) V with a
 // running maximum and sum in fp32, 32 keys at a time: a key per lane for the scores, the
 // head dimension over the lanes for the products with V.
