@@ -314,7 +314,9 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
           for (int k = 0; k < 2; ++k)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              if (ml[k][i].x == -INFINITY) continue;  // no weight there
+              // no weight there. The maximum passes over NaN: a segment of NaN scores alone has
+              // -inf and a sum of NaN, and counts.
+              if (ml[k][i].x == -INFINITY && ml[k][i].y == 0.f) continue;
               const float f = exp2f(ml[k][i].x - mm[i]);
               ll[i] += ml[k][i].y * f;
 #pragma unroll

@@ -1,0 +1,50 @@
+"""The serving operators over a paged cache where values are not finite."""
+import pytest
+import torch
+
+from llama_decoder_block_kv_b200 import binding as B
+from tests import paged_reference as R
+from tests.test_gpu_paged import Paged
+
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+
+
+def put(p, which, at, value, cols=slice(None), request=0):
+    """`value` in columns `cols` of key `at` of a request, in the pages and in the request's own copy."""
+    t, q, k, v = p.seqs[request]
+    b = [i for i, (n, _) in enumerate(p.lens) if n][request]
+    page = p.a.page_size
+    (p.kp if which == "k" else p.vp)[int(p.table[b, at // page]), :, at % page, cols] = value
+    x = (k if which == "k" else v).clone()
+    x[at, :, cols] = value
+    p.seqs[request] = (t, q, x, v) if which == "k" else (t, q, k, x)
+
+
+def same_kinds(p, what=""):
+    """NaN, infinities and finite values stand where the 64-bit form has them, the finite ones within two roundings of
+    the storage type and of P (the bound's weights would be infinite next to infinite values)."""
+    assert B.llama_paged_status(p.st) == (B.LLAMA_OK, 0), what
+    for t, q, k, v in p.seqs:
+        want, _, _ = R.attention(q, k, v)
+        got = p.out[t:t + q.shape[0]].double()
+        assert torch.equal(torch.isnan(got), torch.isnan(want)), (what, t, "NaN")
+        assert torch.equal(got.isposinf(), want.isposinf()) and torch.equal(got.isneginf(), want.isneginf()), (what, t, "inf")
+        fine = torch.isfinite(want)
+        assert ((got - want)[fine].abs() <= 2.0 ** -6 * (want[fine].abs() + 1)).all(), (what, t)
+
+
+# ------------------------------------------------------------------ NaN scores alone in a tile
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("H,Hkv,D", [(4, 2, 64), (4, 4, 64), (8, 2, 128), (16, 1, 128)])
+@pytest.mark.parametrize("n,kv", [(1, 321), (1, 577), (1, 641), (3, 321), (3, 641), (40, 1025)])
+def test_a_nan_key_alone_in_its_tile_reaches_the_row(n, kv, H, Hkv, D, dtype):
+    """The newest key has a key tile, and so a CTA, of its own, and its scores are NaN: the rows that see it are NaN,
+    the others as they would be without it."""
+    p = Paged([(n, kv)], H, Hkv, D, 16, dtype)
+    put(p, "k", kv - 1, NAN)
+    p.call()
+    assert torch.isnan(p.out[n - 1].float()).all()
+    same_kinds(p)
