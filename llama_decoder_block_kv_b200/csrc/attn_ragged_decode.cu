@@ -13,8 +13,8 @@
 //               the request's last one are read as out of range, i.e. zeros;
 //   warps 0..3  warp w takes keys 16 w .. 16 w + 15 of every tile on the warp-level
 //               bf16 MMA (HBM-bound: it keeps up) with its own running maximum, sum
-//               and O; P is split into two bf16 parts (~16 bits kept). At the end of
-//               a segment the four states merge in the ring stage of its last tile.
+//               and O; P is split into two bf16 parts (~16 bits kept, rd_split). At the
+//               end of a segment the four states merge in the ring stage of its last tile.
 // V rows past the last key hold whatever the page holds, and 0 x NaN is NaN in the
 // MMA: the warp that owns them zeroes them in shared memory first.
 //
@@ -90,6 +90,19 @@ __device__ __forceinline__ uint32_t rd_transpose(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+
+// (a, b) >= 0 as hi + lo, pairs of bf16: the upper halves, and the remainders rounded to
+// bf16 (2^-16 of the value kept). Both parts of a weight above zero are above zero, so an
+// infinite V stays infinite in both products: a part rounded to nearest may be zero or
+// negative, and 0 x inf and inf - inf are NaN. 2^-126 in place of a remainder of zero, and as
+// the second part of a weight of zero (whose V row is finite or zeroed, or was seen and makes
+// NaN with the first part), is below what a sum of values can show.
+__device__ __forceinline__ void rd_split(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+  hi = __byte_perm(ua, ub, 0x7632);
+  lo = pack_bf16x2(a - __uint_as_float(ua & 0xffff0000u), b - __uint_as_float(ub & 0xffff0000u));
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x00800080u));
 }
 
 // NARROW (a unit serves at most 8 query heads): the scores are computed as
@@ -286,8 +299,8 @@ __global__ void __launch_bounds__(160, 2)
           // P^T as B fragments (key pairs 2qd (+8), head g), hi + lo bf16 parts:
           // transpose the [key][head] fragments of keys 0-7 and 8-15
           uint32_t h01, l01, h23, l23;
-          split_bf16x2(s[0], s[1], h01, l01);
-          split_bf16x2(s[2], s[3], h23, l23);
+          rd_split(s[0], s[1], h01, l01);
+          rd_split(s[2], s[3], h23, l23);
           const uint32_t bh[2] = {rd_transpose(h01), rd_transpose(h23)};
           const uint32_t bl[2] = {rd_transpose(l01), rd_transpose(l23)};
           // O^T += V^T P^T over this warp's 16 keys; V^T fragments by transposed loads of V
@@ -405,10 +418,10 @@ __global__ void __launch_bounds__(160, 2)
           }
           // O += P V over this warp's 16 keys, P as hi + lo bf16 parts
           uint32_t ph[4], pl[4];
-          split_bf16x2(s[0][0], s[0][1], ph[0], pl[0]);
-          split_bf16x2(s[0][2], s[0][3], ph[1], pl[1]);
-          split_bf16x2(s[1][0], s[1][1], ph[2], pl[2]);
-          split_bf16x2(s[1][2], s[1][3], ph[3], pl[3]);
+          rd_split(s[0][0], s[0][1], ph[0], pl[0]);
+          rd_split(s[0][2], s[0][3], ph[1], pl[1]);
+          rd_split(s[1][0], s[1][1], ph[2], pl[2]);
+          rd_split(s[1][2], s[1][3], ph[3], pl[3]);
 #pragma unroll
           for (int jd = 0; jd < D / 8; jd += 2) {
             const int mi = lane >> 3;

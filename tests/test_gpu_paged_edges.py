@@ -8,7 +8,7 @@ from tests.test_gpu_paged import Paged
 
 pytestmark = pytest.mark.gpu
 
-NAN = float("nan")
+INF, NAN = float("inf"), float("nan")
 
 
 def put(p, which, at, value, cols=slice(None), request=0):
@@ -48,3 +48,21 @@ def test_a_nan_key_alone_in_its_tile_reaches_the_row(n, kv, H, Hkv, D, dtype):
     p.call()
     assert torch.isnan(p.out[n - 1].float()).all()
     same_kinds(p)
+
+
+# ------------------------------------------------------------------ infinite values
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("H,Hkv,D", [(8, 2, 128), (4, 4, 64), (16, 1, 128), (20, 1, 64)])
+@pytest.mark.parametrize("kv,at", [(1, 0), (17, 16), (40, 3), (65, 64), (130, 0), (3000, 1), (3000, 2999)])
+def test_single_tokens_see_infinite_values(kv, at, H, Hkv, D, dtype):
+    """An infinite value of a key that a single token sees is infinite in its row, whatever the key's weight."""
+    p = Paged([(1, kv), (1, 70)], H, Hkv, D, 32, dtype)
+    put(p, "v", at, INF, slice(0, None, 2))
+    put(p, "v", at, -INF, slice(1, None, 4))
+    p.call()
+    same_kinds(p, "one key")
+    if kv > 1:
+        put(p, "v", (at + kv // 2) % kv, INF, slice(0, None, 3))  # meets the first one's signs: NaN there
+        p.call()
+        same_kinds(p, "two keys")
