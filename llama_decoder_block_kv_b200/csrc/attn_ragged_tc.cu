@@ -814,6 +814,7 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
         if (!ok) break;
         if (merger && rows <= RT_FEW && g == 0 && r < rows) bad = (few_bad[r >> 5] >> (r & 31)) & 1;
       }
+      __syncwarp();  // rows that their own threads stored come before the warp's stores to them
       for (unsigned todo = __ballot_sync(0xffffffffu, bad); todo; todo &= todo - 1) {
         const int src = __ffs(todo) - 1;
         ragged_row<bf16, D>(p, w.b, w.s, __shfl_sync(0xffffffffu, tok, src), __shfl_sync(0xffffffffu, h, src), lane);

@@ -66,3 +66,22 @@ def test_single_tokens_see_infinite_values(kv, at, H, Hkv, D, dtype):
         put(p, "v", (at + kv // 2) % kv, INF, slice(0, None, 3))  # meets the first one's signs: NaN there
         p.call()
         same_kinds(p, "two keys")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("H,Hkv,D", [(8, 2, 128), (4, 4, 64), (5, 1, 64), (3, 3, 128)])
+@pytest.mark.parametrize("n,kv", [(2, 2), (40, 40), (130, 130), (300, 300), (300, 1000), (20, 3000), (257, 513)])
+def test_values_that_are_not_finite_at_every_place(n, kv, H, Hkv, D, dtype):
+    """Values that are not finite before the new tokens, among them, at the first and at the last: in whole units and in
+    cut ones, each row has what the keys that it sees give."""
+    places = sorted({0, max(kv - n - 1, 0), kv - n, kv - n + n // 3, kv - n // 2, kv - 2, kv - 1})
+    for i, at in enumerate(places):
+        p = Paged([(n, kv), (1, 65)], H, Hkv, D, 16, dtype, seed=i)
+        put(p, "v", at, (INF, NAN, -INF)[i % 3], slice(i % 3, None, 3))
+        p.call()
+        same_kinds(p, at)
+    p = Paged([(n, kv), (1, 65)], H, Hkv, D, 16, dtype, seed=9)
+    for i, at in enumerate(places):
+        put(p, "v", at, (INF, -INF, NAN)[i % 3], slice(i, None, 5))
+    p.call()
+    same_kinds(p, "all of them")
