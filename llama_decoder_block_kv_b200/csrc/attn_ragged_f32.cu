@@ -19,9 +19,11 @@
 // time there 3 us pass before it knows its range and 3 until its first tile is in, the rest
 // is one or two tiles and the merge of the cut unit.
 //
-// A V row of a later key that is not finite reaches the earlier rows of its tile (0 x
-// NaN): rows whose result is not finite are computed again, key by key (unless their sum
-// is NaN or zero: then a key they see makes the whole row NaN).
+// 0 x NaN and 0 x inf are NaN: where a tile has keys that not every row of the unit sees
+// (at most its last two), the threads look through the V rows of those keys that they
+// copied, put zeros for values that are not finite and note the keys; rows that see such
+// a key add its values at the end (with any weight above zero they are infinite or NaN
+// all the same).
 #include "ragged.cuh"
 
 #include <algorithm>
@@ -51,16 +53,6 @@ __device__ __forceinline__ void rf_copy16(void* dst, const void* src, int bytes)
 __device__ __forceinline__ void rf_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void rf_wait_but_one() { asm volatile("cp.async.wait_group 1;" ::: "memory"); }
 
-// out of line: in line it costs the kernel registers for a path that hardly runs
-template <int D>
-__device__ __noinline__ void rf_row(const RaggedAttnParams& p, int b, int q0, int n_new, int kv, int tok, int h, int lane) {
-  RaggedSeq s;
-  s.q0 = q0;
-  s.n_new = n_new;
-  s.kv = kv;
-  ragged_row<float, D>(p, b, s, tok, h, lane);
-}
-
 template <int D>
 __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
     attn_ragged_f32_kernel(const RaggedAttnParams p, float* __restrict__ part, int* __restrict__ counters, int hpc) {
@@ -74,8 +66,9 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
   __shared__ long long pre[RT_PRE + 1];
   __shared__ long long s_w[3 * RT_PRE / 32];
   __shared__ int s_last;
+  __shared__ unsigned s_odd;  // bit i: the i-th key behind those that every row sees has V values that are not finite
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tx = tid & 15, ty = tid >> 4;
+  const int tid = threadIdx.x, warp = tid >> 5, tx = tid & 15, ty = tid >> 4;
   const int n_rep = p.H / p.Hkv, groups = n_rep / hpc, HG = p.Hkv * groups, bq = RF_ROWS / hpc;
   const int stride = RF_ROWS * D + 2 * RF_ROWS;  // floats of one partial
   const float sl2 = rsqrtf((float)D) * RF_LOG2E;
@@ -91,6 +84,7 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
     // a thread copies 16 bytes of the same column of every LR-th row
     constexpr int LR = RF_THREADS * 4 / D;
     const int lrow = tid / (D / 4), lcol = (tid % (D / 4)) * 4;
+    const int all_see = w.s.kv - w.s.n_new + tok0 + 1;  // keys that every row of the unit sees
     auto load = [&](float* dst, int ld, const void* src, long long row_stride, int j) {
       const float* from = static_cast<const float*>(src) + lcol;
       const int* table = p.tables + (size_t)w.b * p.max_pages;
@@ -116,6 +110,7 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
       rf_commit();
     };
     __syncthreads();  // shared memory of the segment before has been read
+    if (tid == 0) s_odd = 0;
 #pragma unroll
     for (int i = 0; i < RF_ROWS / LR; ++i) {
       const int r = lrow + i * LR, tok = tok0 + r / hpc;
@@ -198,6 +193,20 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
       else
         rf_commit();
       rf_wait_but_one();
+      if ((j + 1) * RF_KT > all_see) {
+#pragma unroll 4
+        for (int i = 0; i < RF_KT / LR; ++i) {
+          const int r = lrow + i * LR, bit = j * RF_KT + r - all_see;
+          float4* at = reinterpret_cast<float4*>(sV + r * D + lcol);
+          const float4 v = *at;
+          const float any = fmaf(v.x, 0.f, v.y * 0.f) + fmaf(v.z, 0.f, v.w * 0.f);  // NaN where one is not finite
+          if (bit >= 0 && !(any == 0.f)) {
+            if (bit < 32) atomicOr(&s_odd, 1u << bit);  // later keys are seen by no row
+            *at = make_float4(fabsf(v.x) < INFINITY ? v.x : 0.f, fabsf(v.y) < INFINITY ? v.y : 0.f,
+                              fabsf(v.z) < INFINITY ? v.z : 0.f, fabsf(v.w) < INFINITY ? v.w : 0.f);
+          }
+        }
+      }
       __syncthreads();  // V(j), P(j) in
       if (live) {
 #pragma unroll 4
@@ -235,7 +244,30 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int c = 0; c < 2 * NC; ++c) rt_split(o2[i][c], o[i][2 * c], o[i][2 * c + 1]);
-    bool bad[4] = {false, false, false, false};  // the row's result is not finite
+    if (s_odd) {
+#pragma unroll 1
+      for (unsigned bits = s_odd; bits; bits &= bits - 1) {
+        const int key = all_see + __ffs(bits) - 1;
+        const float* at = static_cast<const float*>(p.v) + 4 * tx;
+        if (p.tables) {
+          const int page = __ldg(p.tables + (size_t)w.b * p.max_pages + (key >> p.page_shift));
+          if ((unsigned)page >= (unsigned)p.num_pages) continue;
+          at += (size_t)(((page * p.Hkv + kvh) << p.page_shift) + (key & ((1 << p.page_shift) - 1))) * D;
+        } else {
+          at += (size_t)(w.s.q0 + key) * p.v_stride + kvh * D;
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const float4 v = __ldg(reinterpret_cast<const float4*>(at + 64 * c));
+          const float odd[4] = {fabsf(v.x) < INFINITY ? 0.f : v.x, fabsf(v.y) < INFINITY ? 0.f : v.y,
+                                fabsf(v.z) < INFINITY ? 0.f : v.z, fabsf(v.w) < INFINITY ? 0.f : v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][4 * c + e] += key <= last[i] ? odd[e] : 0.f;
+        }
+      }
+    }
     // normalise and store row i of this thread (columns 4 tx + 64 c)
     auto finish = [&](int i, float sum) {
       const int r = 4 * ty + i, tok = tok0 + r / hpc;
@@ -243,10 +275,7 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
       float* dst = static_cast<float*>(p.o) + ((size_t)(w.s.q0 + tok) * p.H + h0 + r % hpc) * D;
       const float inv = 1.f / sum;
 #pragma unroll
-      for (int c = 0; c < 4 * NC; ++c) {
-        o[i][c] = last[i] < 0 ? 0.f : o[i][c] * inv;  // a row without keys is zero
-        bad[i] |= sum > 0.f && !(fabsf(o[i][c]) < INFINITY);
-      }
+      for (int c = 0; c < 4 * NC; ++c) o[i][c] = last[i] < 0 ? 0.f : o[i][c] * inv;  // a row without keys is zero
 #pragma unroll
       for (int c = 0; c < NC; ++c) store4(dst + 64 * c + 4 * tx, o[i] + 4 * c);
     };
@@ -333,17 +362,6 @@ __global__ void __launch_bounds__(RF_THREADS, RfCfg<D>::PER_SM)
         if (tid == 0) counters[c0] = 0;  // re-armed for the next launch
       }
       __syncthreads();  // s_last is written again by the next cut segment
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const unsigned b = __ballot_sync(0xffffffffu, bad[i]);
-#pragma unroll
-      for (int half = 0; half < 2; ++half)
-        if ((b >> (16 * half)) & 0xffffu) {
-          __syncwarp();  // behind the stores above
-          const int r = 8 * warp + 4 * half + i;
-          rf_row<D>(p, w.b, w.s.q0, w.s.n_new, w.s.kv, tok0 + r / hpc, h0 + r % hpc, lane);
-        }
     }
   }
 }

@@ -1,5 +1,5 @@
-// Device parts shared by the attention kernels of packed rows: a request's
-// lengths with their checks, and one row computed by a warp, key by key.
+// Parts shared by the attention kernels of packed rows: a request's lengths with
+// their checks, and the list of key tiles that is cut over the CTAs.
 #pragma once
 
 #include <vector>
@@ -30,69 +30,6 @@ __host__ __device__ __forceinline__ bool ragged_seq(const RaggedAttnParams& p, i
 #endif
   }
   return ok;
-}
-
-// Row tok of the request, query head h, by one warp: softmax(q.k / sqrt(D)) V with a
-// running maximum and sum in fp32, 32 keys at a time: a key per lane for the scores, the
-// head dimension over the lanes for the products with V.
-template <typename T, int D>
-__device__ void ragged_row(const RaggedAttnParams& p, int b, const RaggedSeq& s, int tok, int h, int lane) {
-  constexpr int E = D / 32, PER16 = 16 / sizeof(T);
-  const int kvh = h / (p.H / p.Hkv);
-  const int n = min(s.kv - s.n_new + tok + 1, s.kv);
-  const float scale = rsqrtf((float)D);
-  const size_t row = (size_t)(s.q0 + tok);
-  const T* q = reinterpret_cast<const T*>(p.q) + row * p.q_stride + (size_t)h * D;
-  float o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int j0 = 0; j0 < n; j0 += 32) {
-    const int j = j0 + lane;
-    long long ka = -1, va = -1;  // where the lane's key and value rows begin; -1: rows of zeros
-    if (j < n) {
-      if (p.tables) {
-        const int page = p.tables[(size_t)b * p.max_pages + (j >> p.page_shift)];
-        if ((unsigned)page < (unsigned)p.num_pages)
-          ka = va = ((((long long)page * p.Hkv + kvh) << p.page_shift) + (j & ((1 << p.page_shift) - 1))) * D;
-        else
-          atomicOr(p.status, LLAMA_DEV_PAGE_RANGE);
-      } else {
-        ka = (s.q0 + (long long)j) * p.k_stride + kvh * D;
-        va = (s.q0 + (long long)j) * p.v_stride + kvh * D;
-      }
-    }
-    float dot = 0.f;
-    if (ka >= 0)
-      for (int d = 0; d < D; d += PER16) {
-        const uint4 ku = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p.k) + ka + d);
-        const uint4 qu = *reinterpret_cast<const uint4*>(q + d);
-#pragma unroll
-        for (int e = 0; e < PER16; ++e) dot += to_f32(reinterpret_cast<const T*>(&qu)[e]) * to_f32(reinterpret_cast<const T*>(&ku)[e]);
-      }
-    const float sc = j < n ? dot * scale : -INFINITY;
-    float mt = sc;
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
-    const float mn = fmaxf(m, mt), ref = mn == -INFINITY ? 0.f : mn;
-    const float a = expf(m - ref), w = expf(sc - ref);
-    m = mn;
-    float sum = w;
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    l = l * a + sum;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= a;
-    for (int k = 0; k < min(32, n - j0); ++k) {
-      const float wk = __shfl_sync(0xffffffffu, w, k);
-      const long long at = __shfl_sync(0xffffffffu, va, k);
-      if (at < 0) continue;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] += wk * to_f32(reinterpret_cast<const T*>(p.v)[at + e * 32 + lane]);
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    reinterpret_cast<T*>(p.o)[(row * p.H + h) * D + e * 32 + lane] = from_f32<T>(n > 0 ? o[e] / l : 0.f);
 }
 
 // ---- the list of tiles
