@@ -615,7 +615,9 @@ int llama_block_forward_paged(llama_ctx* ctx, int layer, float* h_dev, const lla
 /*
  * Synchronise the device, return and clear *status_dev: LLAMA_OK or the most
  * severe of LLAMA_ERR_TIMEOUT, LLAMA_ERR_PAGE_RANGE, LLAMA_ERR_OUT_OF_PAGES,
- * LLAMA_ERR_POS_RANGE; *flags (if not NULL) receives the raw bits.
+ * LLAMA_ERR_POS_RANGE; *flags (if not NULL) receives the raw bits. Only the bits
+ * returned are cleared, before the call returns: a flag raised meanwhile or later
+ * is kept. A word that is not the current device's is refused.
  */
 int llama_paged_status(int32_t* status_dev, int* flags);
 

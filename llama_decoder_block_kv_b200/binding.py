@@ -521,9 +521,10 @@ def llama_block_forward_paged(ctx, layer: int, h: torch.Tensor, args: PageArgs, 
 
 
 def llama_paged_status(status: torch.Tensor):
-    """(code, raw bits) of a status word, after synchronising; clears it."""
+    """(code, raw bits) of a status word, after synchronising; clears those bits."""
     flags = ctypes.c_int(0)
-    code = lib().llama_paged_status(_ptr(status), ctypes.byref(flags))
+    p = _whole("status", status, torch.int32, (1,), torch.cuda.current_device())
+    code = lib().llama_paged_status(p, ctypes.byref(flags))
     return code, flags.value
 
 

@@ -37,6 +37,9 @@ int sm_count() {
   return n;
 }
 
+// the flags that a status call has returned, and no others: more may be raised meanwhile
+__global__ void clear_flags_kernel(int* status, int flags) { atomicAnd(status, ~flags); }
+
 }  // namespace
 
 namespace llama {
@@ -208,10 +211,18 @@ int llama_attn_packed(int dtype, int n_heads, int n_kv_heads, int head_dim, cons
 int llama_paged_status(int32_t* status, int* flags) {
   if (flags) *flags = 0;
   if (!status) return LLAMA_ERR_INVALID_ARGS;
+  cudaPointerAttributes at;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaPointerGetAttributes(&at, status) != cudaSuccess) return LLAMA_ERR_CUDA;
+  if (at.type == cudaMemoryTypeUnregistered || (at.type == cudaMemoryTypeDevice && at.device != dev)) return LLAMA_ERR_INVALID_ARGS;
   int w = 0;
-  if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpy(&w, status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess ||
-      cudaMemset(status, 0, sizeof(int)) != cudaSuccess)
+  if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpy(&w, status, sizeof(int), cudaMemcpyDefault) != cudaSuccess)
     return LLAMA_ERR_CUDA;
+  if (w) {
+    // done before this returns: streams that do not wait for the default one may raise flags right after
+    clear_flags_kernel<<<1, 1>>>(status, w);
+    if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(nullptr) != cudaSuccess) return LLAMA_ERR_CUDA;
+  }
   if (flags) *flags = w;
   if (w & LLAMA_DEV_TIMEOUT) return LLAMA_ERR_TIMEOUT;
   if (w & LLAMA_DEV_PAGE_RANGE) return LLAMA_ERR_PAGE_RANGE;

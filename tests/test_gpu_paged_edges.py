@@ -1,4 +1,7 @@
-"""The serving operators over a paged cache where values are not finite."""
+"""The serving operators over a paged cache where values are not finite and calls overlap."""
+import threading
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -163,3 +166,47 @@ def test_values_that_are_not_finite_over_a_very_long_history(dtype):
     p.out[n - 1, :, 9] = 0
     want[n:], p.out[n:] = 0, 0
     assert torch.equal(p.out, want)
+
+
+# ------------------------------------------------------------------ the status word
+
+def test_a_flag_raised_right_after_a_status_call_is_kept():
+    """Another thread keeps the default stream busy, so that whatever a status call leaves running there runs late: a flag
+    that the next call raises on a stream of its own must still stand."""
+    a = B.PageArgs(1, 1, 64, 16, 4, 2)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    lens, new, table, free = ints([0]), ints([1]), torch.zeros((1, 2), **i32), torch.zeros(4, **i32)
+    none, c_out, cu, kv, pos, slot = ints([0]), ints([0]), torch.zeros(2, **i32), torch.zeros(1, **i32), torch.zeros(4, **i32), torch.zeros(4, **i32)
+    st, side, done = status_word(), torch.cuda.Stream(), threading.Event()
+    torch.cuda.synchronize()
+
+    def busy():
+        while not done.is_set():
+            for _ in range(3):
+                torch.cuda._sleep(150_000)
+            time.sleep(2.4e-4)
+
+    other = threading.Thread(target=busy)
+    other.start()
+    try:
+        for i in range(4000):  # a clear that runs late lost about one flag in 80
+            B.llama_paged_status(st)
+            # no page is free: the plan is refused with a flag
+            B.llama_page_plan(a, lens, new, table, free, none, c_out, cu, kv, pos, slot, st, stream=side)
+            side.synchronize()
+            assert B.llama_paged_status(st) == (B.LLAMA_ERR_OUT_OF_PAGES, 16), i
+    finally:
+        done.set()
+        other.join()
+        torch.cuda.synchronize()
+
+
+def test_the_status_word_is_the_current_devices():
+    for bad in (torch.zeros(1, dtype=torch.int32), torch.zeros(1, dtype=torch.int64, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")):
+        with pytest.raises(ValueError):
+            B.llama_paged_status(bad)
+    host = torch.ones(1, dtype=torch.int32)
+    assert B.lib().llama_paged_status(host.data_ptr(), None) == B.LLAMA_ERR_INVALID_ARGS and int(host) == 1
+    st = status_word()
+    st.fill_(2 + 8)
+    assert B.llama_paged_status(st) == (B.LLAMA_ERR_PAGE_RANGE, 10) and int(st) == 0
