@@ -360,6 +360,9 @@ class PageArgs:
         object.__setattr__(self, name, value)
         self.__dict__.pop("_ref", None)
 
+    def __getstate__(self):  # copies and pickles hold the values alone
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+
     def ref(self):
         """Reference to the C structure, built once for these values."""
         r = self.__dict__.get("_ref")

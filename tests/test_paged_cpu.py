@@ -1,6 +1,8 @@
 """CPU checks of the paged serving operators: what the C calls refuse before any launch, and the plain forms the GPU tests use."""
+import copy
 import ctypes
 import os
+import pickle
 
 import numpy as np
 import pytest
@@ -129,3 +131,12 @@ def test_attention_lists_cover_every_tile_once(M, H, Hkv):
     for S in (1, 130, 8192):
         for sms in (148, 7):
             assert B.lib().llama_selfcheck_plans(M, H * 64, H, Hkv, 1024, S, sms) == B.LLAMA_OK, (M, H, Hkv, S, sms)
+
+
+def test_page_args_are_copied_and_pickled_after_use():
+    a = B.PageArgs(**GOOD)
+    a.ref()
+    for b in (copy.copy(a), copy.deepcopy(a), pickle.loads(pickle.dumps(a))):
+        assert b == a and b.ref() is not a.ref()
+        b.num_pages += 1  # each with a C structure of its own
+        assert b.ref()._obj.num_pages == a.ref()._obj.num_pages + 1 == a.num_pages + 1
