@@ -601,7 +601,8 @@ int llama_attn_packed(int dtype, int n_heads, int n_kv_heads, int head_dim, cons
  * context's heads, head_dim and dtype. Rows of tokens with slot -1 are unspecified
  * afterwards. workspace_dev: llama_block_paged_workspace_bytes(ctx, n_tokens) bytes, zeroed
  * once, under the rules of llama_attn_workspace_bytes; one workspace serves all layers of a
- * step. Runs on the context's device; the first call of more tokens than reserved
+ * step. Runs on the context's device, which the tensors are on (an h_dev that is not is
+ * refused) and which is the current one afterwards; the first call of more tokens than reserved
  * (llama_reserve) allocates, so reserve before a capture. Like the context's other calls,
  * not to be overlapped with another call of the same context.
  */

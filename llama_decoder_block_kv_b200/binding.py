@@ -336,7 +336,8 @@ def llama_linear_noalloc_status():
 
 
 # ---- serving operators over a paged cache. Their calls run on the current
-# device, so tensors of another device (or of the CPU) are refused here.
+# device (the block's on its context's), so tensors of another device (or of the
+# CPU) are refused here.
 _TORCH = {"fp32": torch.float32, "bf16": torch.bfloat16}
 _CODE = {torch.float32: LLAMA_FP32, torch.bfloat16: LLAMA_BF16}
 
@@ -385,7 +386,7 @@ def _raw_stream(stream, device: int) -> int:
 
 def _on_device(name: str, t: torch.Tensor, dtype, device: int) -> int:
     if not t.is_cuda or t.get_device() != device:
-        raise ValueError(f"{name} must be on the current device cuda:{device}, got {t.device}")
+        raise ValueError(f"{name} must be on the call's device cuda:{device}, got {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     return t.data_ptr()
@@ -510,8 +511,11 @@ def llama_block_forward_paged(ctx, layer: int, h: torch.Tensor, args: PageArgs, 
                               v_pages: torch.Tensor, block_tables: torch.Tensor, cu: torch.Tensor, kv_lens: torch.Tensor,
                               positions: torch.Tensor, slots: torch.Tensor, max_new: int, workspace: torch.Tensor,
                               status: torch.Tensor, stream=None) -> None:
-    """h fp32 [n][dim] in place; the other tensors as in llama_rope_append and llama_attn_paged, on one device."""
-    d, i32, dt = torch.cuda.current_device(), torch.int32, _TORCH[args.dtype]
+    """h fp32 [n][dim] in place; the other tensors as in llama_rope_append and llama_attn_paged, all on the context's
+    device, whatever the current one is."""
+    if not h.is_cuda:
+        raise ValueError(f"h must be on the context's device, got {h.device}")
+    d, i32, dt = h.get_device(), torch.int32, _TORCH[args.dtype]
     n, B = h.shape[0], kv_lens.shape[0]
     pool = (args.num_pages, args.n_kv_heads, args.page_size, args.head_dim)
     _check(lib().llama_block_forward_paged(

@@ -767,6 +767,11 @@ int llama_block_forward_paged(llama_ctx* c, int layer, float* h, const llama_pag
       !aligned(status, 4) || workspace_bytes < llama_block_paged_workspace_bytes(c, n_tokens))
     return LLAMA_ERR_INVALID_ARGS;
   if (!c->layers[layer].set) return LLAMA_ERR_NOT_READY;
+  // tensors of another device (or of the host) would be read by this one's kernels
+  cudaPointerAttributes at;
+  if (cudaPointerGetAttributes(&at, h) != cudaSuccess) return LLAMA_ERR_CUDA;
+  if (at.type == cudaMemoryTypeUnregistered || (at.type == cudaMemoryTypeDevice && at.device != c->device))
+    return LLAMA_ERR_INVALID_ARGS;
   if (cudaSetDevice(c->device) != cudaSuccess) return LLAMA_ERR_CUDA;
   int r;
   if ((r = reserve(c, n_tokens))) return r;

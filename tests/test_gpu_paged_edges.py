@@ -210,3 +210,63 @@ def test_the_status_word_is_the_current_devices():
     st = status_word()
     st.fill_(2 + 8)
     assert B.llama_paged_status(st) == (B.LLAMA_ERR_PAGE_RANGE, 10) and int(st) == 0
+
+
+# ------------------------------------------------------------------ a block over a paged cache
+
+def block_workload(act, **kw):
+    import oracle as O
+    from llama_decoder_block_kv_b200 import synth
+
+    return synth.Workload(**(dict(name="paged block edges", dim=256, n_layers=1, n_heads=4, n_kv_heads=2, ffn_hidden=O.ffn_hidden_dim(256, 256),
+                                  vocab_size=0, multiple_of=256, ffn_dim_multiplier=None, norm_eps=1e-5, rope_theta=10000.0,
+                                  max_batch_size=1, max_seq_len=64, act=act, batch=1, seed=9, norm_weights="random") | kw))
+
+
+class Block:
+    """One request's tokens through a paged block: its pages, tables and a call."""
+
+    def __init__(self, w, ctx, n):
+        from llama_decoder_block_kv_b200 import synth
+
+        self.ctx, self.a = ctx, B.PageArgs(w.n_heads, w.n_kv_heads, w.head_dim, 16, 8, 4, w.act)
+        self.h = synth.hidden(w, (1, n, w.dim), call=1)[0].to("cuda").contiguous()
+        self.kp, self.vp = (torch.zeros((8, w.n_kv_heads, 16, w.head_dim), dtype=DT[w.act], device="cuda") for _ in range(2))
+        self.table, self.cu, self.kv = ints([[5, 2, 7, 0]]), ints([0, n]), ints([n])
+        self.pos, self.slot = ints(list(range(n))), ints([(5, 2, 7, 0)[i // 16] * 16 + i % 16 for i in range(n)])
+        self.ws = torch.zeros(B.llama_block_paged_workspace_bytes(ctx, n), dtype=torch.uint8, device="cuda")
+        self.st, self.n = status_word(), n
+
+    def call(self, **kw):
+        x = dict(h=self.h, table=self.table) | kw
+        B.llama_block_forward_paged(self.ctx, 0, x["h"], self.a, self.kp, self.vp, x["table"], self.cu, self.kv, self.pos, self.slot, self.n,
+                                    self.ws, self.st)
+
+
+def test_a_block_runs_on_its_contexts_device(monkeypatch):
+    """The tensors' device counts, not the current one; tensors that are not on the context's device are refused."""
+    import ctypes
+
+    from tests.gpu_util import Pair
+
+    w = block_workload("bf16")
+    pair = Pair(w)
+    try:
+        want = Block(w, pair.ctx, 20)
+        want.call()
+        b = Block(w, pair.ctx, 20)
+        with monkeypatch.context() as m:
+            m.setattr(torch.cuda, "current_device", lambda: torch.cuda.device_count())
+            b.call()
+            for kw in (dict(h=b.h.cpu()), dict(table=b.table.cpu())):
+                with pytest.raises(ValueError):
+                    b.call(**kw)
+        torch.cuda.synchronize()
+        assert torch.equal(b.h, want.h) and torch.equal(b.kp, want.kp) and torch.equal(b.vp, want.vp)
+        host = torch.zeros((20, w.dim))
+        code = B.lib().llama_block_forward_paged(
+            pair.ctx, 0, ctypes.c_void_p(host.data_ptr()), b.a.ref(), *[x.data_ptr() for x in (b.kp, b.vp, b.table, b.cu, b.kv, b.pos, b.slot)],
+            1, 20, 20, b.ws.data_ptr(), b.ws.numel(), b.st.data_ptr(), None)
+        assert code == B.LLAMA_ERR_INVALID_ARGS and (host == 0).all()
+    finally:
+        pair.close()
