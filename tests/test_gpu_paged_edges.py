@@ -1,4 +1,4 @@
-"""The serving operators over a paged cache where values are not finite and calls overlap."""
+"""The serving operators over a paged cache where values are not finite, lengths are malformed and calls overlap."""
 import threading
 import time
 
@@ -212,6 +212,27 @@ def test_the_status_word_is_the_current_devices():
     assert B.llama_paged_status(st) == (B.LLAMA_ERR_PAGE_RANGE, 10) and int(st) == 0
 
 
+# ------------------------------------------------------------------ malformed lengths
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n", [1, 6])
+def test_malformed_starts_leave_rows_alone(n, dtype):
+    """Whatever cu holds, only the rows of requests with valid bounds are written, with their own values."""
+    p = Paged([(n, 40), (n, 33), (n, 300)], 4, 2, 64, 16, dtype)
+    N = 3 * n
+    q_all, hist = p.q, [(k, v) for _, _, k, v in p.seqs]
+    rows = p.out.shape[0]
+    for cu in ([0, n, n - 1, N], [0, n, 10 ** 6, 10 ** 6], [-5, n, n, N], [2 ** 31 - 1, -2 ** 31, 0, 0], [0, N, n, 2 * n],
+               [0, n, 2 * n, rows + 1], [0, 0, -1, N], [n, 0, n, 2 * n]):
+        p.cu.copy_(ints(cu))
+        p.out.fill_(LEFT)
+        p.call(max_new=n)
+        good = [0 <= a <= b <= rows and b - a <= n for a, b in zip(cu, cu[1:])]
+        assert not all(good)
+        assert B.llama_paged_status(p.st) == (B.LLAMA_ERR_POS_RANGE, 2), cu
+        check_attention(p.out, [(a, q_all[a:b], *hist[i]) for i, (a, b) in enumerate(zip(cu, cu[1:])) if good[i] and b > a], p.dt, cu)
+
+
 # ------------------------------------------------------------------ a block over a paged cache
 
 def block_workload(act, **kw):
@@ -269,4 +290,30 @@ def test_a_block_runs_on_its_contexts_device(monkeypatch):
             1, 20, 20, b.ws.data_ptr(), b.ws.numel(), b.st.data_ptr(), None)
         assert code == B.LLAMA_ERR_INVALID_ARGS and (host == 0).all()
     finally:
+        pair.close()
+
+
+@pytest.mark.parametrize("act", ["fp32", "bf16"])
+def test_pages_of_a_half_split_block_hold_interleaved_pairs(act):
+    """The same weights given in the half-split order: the same hidden states and the same pages, bit by bit."""
+    import dataclasses
+
+    from llama_decoder_block_kv_b200 import synth
+    from tests.gpu_util import Pair
+    from tests.test_gpu_rope_half_split import _to_half_split
+
+    w = block_workload(act)
+    lw = synth.layer_weights(w, 0, device="cpu")
+    lw["wq"], lw["wk"] = (_to_half_split(lw[k], n, w.head_dim) for k, n in (("wq", w.n_heads), ("wk", w.n_kv_heads)))
+    pair, half = Pair(w), B.Llama(dataclasses.replace(B.ModelArgs.from_workload(w), rope_half_split=True))
+    try:
+        B.llama_set_layer(half.ctx, 0, {k: v.cuda().contiguous() for k, v in lw.items()})
+        a, b = Block(w, pair.ctx, 40), Block(w, half.ctx, 40)
+        for x in (a, b):
+            x.call()
+            assert B.llama_paged_status(x.st) == (B.LLAMA_OK, 0)
+        assert torch.equal(a.h, b.h) and torch.equal(a.kp, b.kp) and torch.equal(a.vp, b.vp)
+        assert (a.kp[[5, 2]] != 0).any(-1).all() and (a.kp[7, :, :8] != 0).any(-1).all() and not a.kp[[0, 1, 3, 4, 6]].any()
+    finally:
+        half.close()
         pair.close()

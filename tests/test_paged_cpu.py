@@ -140,3 +140,11 @@ def test_page_args_are_copied_and_pickled_after_use():
         assert b == a and b.ref() is not a.ref()
         b.num_pages += 1  # each with a C structure of its own
         assert b.ref()._obj.num_pages == a.ref()._obj.num_pages + 1 == a.num_pages + 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_workspace_serves_every_head_layout(D, dtype):
+    """Its size follows from dtype and head_dim alone: layers and models of other head counts share it."""
+    sizes = {B.llama_attn_workspace_bytes(H, Hkv, D, dtype) for H, Hkv in ((1, 1), (4, 2), (32, 8), (64, 8), (20, 1), (17, 1), (1 << 16, 1))}
+    assert len(sizes) == 1 and min(sizes) > 0
