@@ -482,7 +482,8 @@ int llama_linear_noalloc_status(int* flags);
  *    read or written, whatever the lengths, tables and slots hold.
  *  - row strides are in elements, at least the row's width, and multiples of
  *    16 bytes; tensors start on 16-byte boundaries; inputs and outputs do not
- *    overlap except where a call says so. n_seqs <= LLAMA_MAX_SEQS.
+ *    overlap except where a call says so. 1 <= n_seqs <= LLAMA_MAX_SEQS; at least
+ *    one token (a step without tokens needs no call), at most 2^31 - 256.
  */
 #define LLAMA_MAX_SEQS 4096
 
@@ -490,7 +491,7 @@ int llama_linear_noalloc_status(int* flags);
  * Shape of a paged cache. Rules: dtype LLAMA_FP32 or LLAMA_BF16; n_heads a
  * multiple of n_kv_heads; head_dim 64 or 128; page_size 16, 32, 64 or 128
  * tokens; num_pages >= 1 with num_pages * n_kv_heads * page_size < 2^31;
- * max_pages >= 1 (columns of block_tables) with max_pages * page_size < 2^31.
+ * max_pages >= 1 (columns of block_tables) with max_pages * page_size <= 2^31 - 256.
  */
 typedef struct {
   int32_t dtype;

@@ -15,9 +15,12 @@ bool heads_ok(int dtype, int H, int Hkv, int D) {
          (D == 64 || D == 128);
 }
 
+// Keys of a request and tokens of a call: the kernels' tiles and units go past them by up to 255 in 32 bits
+constexpr long long MAX_LEN = (1LL << 31) - 256;
+
 bool pool_ok(const llama_page_args* a) {
   return a && page_shift(a->page_size) > 0 && a->num_pages >= 1 && a->max_pages >= 1 &&
-         (long long)a->max_pages * a->page_size < (1LL << 31) && (long long)a->num_pages * a->page_size < (1LL << 31);
+         (long long)a->max_pages * a->page_size <= MAX_LEN && (long long)a->num_pages * a->page_size < (1LL << 31);
 }
 
 bool stride_ok(int64_t stride, int64_t width, int esz) {
@@ -144,7 +147,7 @@ int llama_attn_paged(const llama_page_args* a, const void* q, int64_t q_stride, 
                      const void* v_pages, const int32_t* tables, const int32_t* cu, const int32_t* kv_lens, int n_seqs,
                      int n_tokens, int max_new, void* out, void* workspace, int64_t workspace_bytes, int32_t* status,
                      void* stream) {
-  if (!page_args_ok(a) || n_seqs < 1 || n_seqs > LLAMA_MAX_SEQS || n_tokens < 1 || max_new < 1)
+  if (!page_args_ok(a) || n_seqs < 1 || n_seqs > LLAMA_MAX_SEQS || n_tokens < 1 || n_tokens > MAX_LEN || max_new < 1)
     return LLAMA_ERR_INVALID_ARGS;
   if (!stride_ok(q_stride, (int64_t)a->n_heads * a->head_dim, a->dtype == LLAMA_BF16 ? 2 : 4))
     return LLAMA_ERR_INVALID_ARGS;
@@ -179,7 +182,7 @@ int llama_attn_packed(int dtype, int n_heads, int n_kv_heads, int head_dim, cons
                       int n_tokens, int max_len, void* out, void* workspace, int64_t workspace_bytes, int32_t* status,
                       void* stream) {
   if (!heads_ok(dtype, n_heads, n_kv_heads, head_dim) || n_seqs < 1 || n_seqs > LLAMA_MAX_SEQS || n_tokens < 1 ||
-      max_len < 1)
+      n_tokens > MAX_LEN || max_len < 1)
     return LLAMA_ERR_INVALID_ARGS;
   const int esz = dtype == LLAMA_BF16 ? 2 : 4;
   const int64_t kw = (int64_t)n_kv_heads * head_dim;

@@ -761,7 +761,7 @@ int llama_block_forward_paged(llama_ctx* c, int layer, float* h, const llama_pag
   if (!c || layer < 0 || layer >= c->L || !page_args_ok(a)) return LLAMA_ERR_INVALID_ARGS;
   if (a->dtype != (c->bf16 ? LLAMA_BF16 : LLAMA_FP32) || a->n_heads != c->H || a->n_kv_heads != c->Hkv || a->head_dim != c->D)
     return LLAMA_ERR_INVALID_ARGS;
-  if (n_seqs < 1 || n_seqs > LLAMA_MAX_SEQS || n_tokens < 1 || max_new < 1) return LLAMA_ERR_INVALID_ARGS;
+  if (n_seqs < 1 || n_seqs > LLAMA_MAX_SEQS || n_tokens < 1 || n_tokens > INT32_MAX - 255 || max_new < 1) return LLAMA_ERR_INVALID_ARGS;
   if (!aligned(h, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(tables, 4) || !aligned(cu, 4) ||
       !aligned(kv_lens, 4) || !aligned(positions, 4) || !aligned(slots, 4) || !aligned(workspace, 256) ||
       !aligned(status, 4) || workspace_bytes < llama_block_paged_workspace_bytes(c, n_tokens))

@@ -148,3 +148,15 @@ def test_one_workspace_serves_every_head_layout(D, dtype):
     """Its size follows from dtype and head_dim alone: layers and models of other head counts share it."""
     sizes = {B.llama_attn_workspace_bytes(H, Hkv, D, dtype) for H, Hkv in ((1, 1), (4, 2), (32, 8), (64, 8), (20, 1), (17, 1), (1 << 16, 1))}
     assert len(sizes) == 1 and min(sizes) > 0
+
+
+def test_lengths_whose_tiles_would_pass_32_bits_are_refused():
+    """A request's last key tile and a call's last unit of rows end up to 255 past its keys and tokens."""
+    bad = B.LLAMA_ERR_INVALID_ARGS
+    for page in (16, 128):
+        most = (2 ** 31 - 256) // page
+        for k in range(1, 256 // page):
+            a = page_args(max_pages=most + k, page_size=page)
+            assert plan(a) == append(a) == paged(a) == bad
+    for n in (2 ** 31 - 255, 2 ** 31 - 1):
+        assert paged(page_args(), n=n) == packed(n=n) == bad
