@@ -575,6 +575,15 @@ int64_t llama_attn_workspace_bytes(int dtype, int n_heads, int n_kv_heads, int h
  * position range flag; a table entry outside the pool raises the page range
  * flag and counts as keys and values of zero. The order of sums depends on the
  * lengths only: equal calls give equal bits.
+ * Weights: fp32 keeps them in 32 bits. bf16 keeps about 16 bits of each weight
+ * in the product with V in calls of single tokens (max_new 1), and rounds it to
+ * bf16 (off by at most 2^-8 of it) in the others, which adds about as much to the
+ * error as the rounding of the output; the sum that divides them is fp32, of the
+ * unrounded weights. So the last bits of a token's row depend on whether a request
+ * of the same call has more than one new token.
+ * NaN and infinities in a key or value reach the rows that see it, as in the
+ * formula, and no others. The product with V is summed before the division, with
+ * weights of up to 2^8 (bf16) or 1: |V| near the largest fp32 value may overflow.
  */
 int llama_attn_paged(const llama_page_args* args, const void* q_dev, int64_t q_stride, const void* k_pages_dev,
                      const void* v_pages_dev, const int32_t* block_tables_dev, const int32_t* cu_dev,
@@ -602,7 +611,8 @@ int llama_attn_packed(int dtype, int n_heads, int n_kv_heads, int head_dim, cons
  * context's heads, head_dim and dtype. Rows of tokens with slot -1 are unspecified
  * afterwards. workspace_dev: llama_block_paged_workspace_bytes(ctx, n_tokens) bytes, zeroed
  * once, under the rules of llama_attn_workspace_bytes; one workspace serves all layers of a
- * step. Runs on the context's device, which the tensors are on (an h_dev that is not is
+ * step. status_dev has the flags of the paged calls alone; waits of the linears report
+ * through llama_get_error. Runs on the context's device, which the tensors are on (an h_dev that is not is
  * refused) and which is the current one afterwards; the first call of more tokens than reserved
  * (llama_reserve) allocates, so reserve before a capture. Like the context's other calls,
  * not to be overlapped with another call of the same context.

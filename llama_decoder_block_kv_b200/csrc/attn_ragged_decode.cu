@@ -21,6 +21,11 @@
 // Measured: 32 requests of 1024..8128 tokens at 32/8 heads (497 MB) 89 us, 5.6 TB/s, 85 %
 // of a copy; one request of some 600 tokens at 32 heads 9.4 us, bound by the chain
 // lengths, table, tiles, partials, merge.
+//
+// A CTA keeps 12 bytes of shared memory per request. At head_dim 128 that leaves room for two
+// CTAs per SM up to about 1300 requests; beyond them one is resident, and half the bytes are
+// in flight: 1.2 M keys of 2 kv heads in 1290 requests 219 us (5.6 TB/s), in 1320 322 us
+// (3.8), in 3900 391 us (3.1). At head_dim 64 two always fit (246, 242 and 276 us).
 #include "ragged.cuh"
 
 #include <algorithm>
@@ -93,7 +98,7 @@ __device__ __forceinline__ uint32_t rd_transpose(uint32_t x) {
 }
 
 // (a, b) >= 0 as hi + lo, pairs of bf16: the upper halves, and the remainders rounded to
-// bf16 (2^-16 of the value kept). Both parts of a weight above zero are above zero, so an
+// bf16 (the sum is off by at most 2^-16 of the value). Both parts of a weight above zero are above zero, so an
 // infinite V stays infinite in both products: a part rounded to nearest may be zero or
 // negative, and 0 x inf and inf - inf are NaN. 2^-126 in place of a remainder of zero, and as
 // the second part of a weight of zero (whose V row is finite or zeroed, or was seen and makes

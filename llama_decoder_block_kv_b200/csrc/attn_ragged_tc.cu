@@ -35,10 +35,13 @@
 // last MMA of a group to its commit pass another 420 cycles, so a tile's chain
 // is about 1000 cycles of tensor core and 1700 of softmax, and A and B together
 // reach 2500 to 3000 cycles per pair of tiles where the MMAs alone would take
-// 2057. One prompt of 8192 tokens at 32/8 heads of 128: 464 us, 1185 TFLOP/s.
+// 2057. One prompt of 8192 tokens at 32/8 heads of 128: 468 us, 1175 TFLOP/s in a
+// short burst; four of them 2.22 ms, 990 TFLOP/s, under the power limit (1.89 ms in
+// single calls apart).
 // Short prompts add what a unit costs besides its tiles (Q, the first S, the
 // last P V, the way out of O: about 5 us, partly under its neighbours' work):
-// 16 prompts of 17..2047 tokens at 32 heads 285 us. Measured on the way:
+// 16 prompts of 17..2047 tokens at 32 heads 290 us in a short burst, 339 us call after
+// call on new inputs. Measured on the way (bursts):
 //  - one issuing thread picked by its lane number in place of elect.sync, and
 //    one for both tiles: 635 us for the long prompt, 8 MMAs taking 423 cycles
 //    to issue;
@@ -54,8 +57,12 @@
 // 2^8 (O and the sum are then rescaled), so P <= 2^8.
 //
 // P is rounded to one bf16 for the product with V (fp32 sum of the unrounded
-// values): a second part of the remainder would raise the MMA work by half and
-// take the error from 1.4 to 1.0 times that of rounding the output alone.
+// values). Against the 64-bit form that leaves 2.0 to 2.3e-3 (relative, over all
+// values) where rounding the output alone leaves 1.6 to 1.66e-3. With a second part of
+// the remainder, as the contiguous prefill kernels have (attn_tc.cu), it is 1.6 to
+// 1.66e-3, but the MMA work rises by half and the softmax has to make the parts: 8192
+// tokens 468 -> 602 us (652 us there), ragged prompts 290 -> 421, chunks 171 -> 219, a mixed
+// step 172 -> 213. The header states the rounding.
 //
 // V rows past the request's last key hold whatever the page or the next prompt
 // holds; 0 x NaN is NaN in the MMA, so the softmax threads zero those rows of

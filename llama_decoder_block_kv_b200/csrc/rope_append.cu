@@ -6,7 +6,7 @@
 // to 2^s threads of one block; a thread moves 8 consecutive values (16 or 32 bytes) at
 // the same place of up to three heads, so its angles are read once, and issues all its
 // loads before it waits for the first. 8 thousand tokens at 64/8 heads of 128 (bf16,
-// 312 MB): 60 us, 5.2 TB/s; one thread per 8 values of the whole call: 86 us.
+// 312 MB): 62 us, 5.0 TB/s (one thread per 8 values of the whole call: 86 us).
 #include "kernels.cuh"
 
 namespace llama {
