@@ -100,14 +100,15 @@ __device__ __forceinline__ uint32_t rd_transpose(uint32_t x) {
 // (a, b) >= 0 as hi + lo, pairs of bf16: the upper halves, and the remainders rounded to
 // bf16 (the sum is off by at most 2^-16 of the value). Both parts of a weight above zero are above zero, so an
 // infinite V stays infinite in both products: a part rounded to nearest may be zero or
-// negative, and 0 x inf and inf - inf are NaN. 2^-126 in place of a remainder of zero, and as
-// the second part of a weight of zero (whose V row is finite or zeroed, or was seen and makes
-// NaN with the first part), is below what a sum of values can show.
+// negative, and 0 x inf and inf - inf are NaN. 2^-126 stands in for a remainder of zero, below
+// what a sum of such values shows; a weight of zero stays zero.
 __device__ __forceinline__ void rd_split(float a, float b, uint32_t& hi, uint32_t& lo) {
   const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
   hi = __byte_perm(ua, ub, 0x7632);
   lo = pack_bf16x2(a - __uint_as_float(ua & 0xffff0000u), b - __uint_as_float(ub & 0xffff0000u));
-  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x00800080u));
+  uint32_t least;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(least) : "r"(hi), "r"(0x00800080u));
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(lo) : "r"(least));
 }
 
 // NARROW (a unit serves at most 8 query heads): the scores are computed as

@@ -93,6 +93,26 @@ def test_values_that_are_not_finite_at_every_place(n, kv, H, Hkv, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("H,Hkv,D", [(8, 2, 128), (4, 4, 64), (16, 1, 128), (20, 1, 64)])
+@pytest.mark.parametrize("n", [1, 5])
+def test_huge_values_of_no_weight_count_nothing(n, H, Hkv, D, dtype):
+    """Values near the type's largest under keys whose weight is zero in fp32 (scores 256 below the others)."""
+    kv = 150
+    p = Paged([(n, kv)], H, Hkv, D, 16, dtype)
+    p.wide.fill_(8.0)
+    p.kp.fill_(4.0 * (64 / D) ** 0.5)  # scores of 256
+    p.vp.fill_(1.0)
+    for at in (0, 3, 70, 129, kv - n - 1):
+        page, off = int(p.table[0, at // 16]), at % 16
+        p.kp[page, :, off], p.vp[page, :, off] = 0, 3e38
+    p.call()
+    assert B.llama_paged_status(p.st) == (B.LLAMA_OK, 0)
+    # Weights of 1 and 0: whole numbers times their own reciprocals, two roundings of 2^-24, (1 + 2^-24)^2 - 1 < 2^-22;
+    # in bf16 the nearest value is 1.
+    assert ((p.out[:n].double() - 1).abs() <= (2.0 ** -22 if dtype == "fp32" else 0)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_packed_values_that_are_not_finite(dtype):
     """The same over packed rows, K and V slices of one matrix, in the middle of a batch."""
     H, Hkv, D, lens = 8, 2, 128, [33, 290, 5]
