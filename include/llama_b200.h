@@ -582,8 +582,8 @@ int64_t llama_attn_workspace_bytes(int dtype, int n_heads, int n_kv_heads, int h
  * unrounded weights. So the last bits of a token's row depend on whether a request
  * of the same call has more than one new token.
  * NaN and infinities in a key or value reach the rows that see it, as in the
- * formula, and no others. The product with V is summed before the division, with
- * weights of up to 2^8 (bf16) or 1: |V| near the largest fp32 value may overflow.
+ * formula, and no others. The product with V is summed in fp32 before the division,
+ * with weights of at most 1: values near the largest ones of several keys overflow.
  */
 int llama_attn_paged(const llama_page_args* args, const void* q_dev, int64_t q_stride, const void* k_pages_dev,
                      const void* v_pages_dev, const int32_t* block_tables_dev, const int32_t* cu_dev,

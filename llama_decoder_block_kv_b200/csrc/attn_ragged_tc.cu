@@ -54,7 +54,7 @@
 //  - rows stored by their own threads: 509 us against 484.
 //
 // A thread raises its running maximum only when a score passes it by more than
-// 2^8 (O and the sum are then rescaled), so P <= 2^8.
+// 2^8 (O and the sum are then rescaled), and takes its weights 2^8 below it, so P <= 1.
 //
 // P is rounded to one bf16 for the product with V (fp32 sum of the unrounded
 // values). Against the 64-bit form that leaves 2.0 to 2.3e-3 (relative, over all
@@ -737,8 +737,8 @@ __global__ void __launch_bounds__(RT_THREADS, 1)
               }
               m_used = m_new;
             }
-            const float m_ref = m_used == -INFINITY ? 0.f : m_used;
-            const uint64_t negm2 = rt_f2(-m_ref, -m_ref);
+            const float m_ref = m_used == -INFINITY ? 0.f : -RT_RESCALE - m_used;
+            const uint64_t negm2 = rt_f2(m_ref, m_ref);
             uint64_t ls[2] = {rt_f2(0.f, 0.f), rt_f2(0.f, 0.f)};
             auto weights = [&](int c0) {
               uint32_t pp[16];

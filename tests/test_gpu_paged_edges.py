@@ -113,6 +113,26 @@ def test_huge_values_of_no_weight_count_nothing(n, H, Hkv, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,kv", [(1, 300), (5, 300), (140, 400), (3, 3000)])
+def test_a_huge_value_under_a_score_somewhat_above_the_others(n, kv, dtype):
+    """One key scores 5 (7.2 in powers of two) above the others, which come before and behind it, and holds values of 3e36: its
+    weight times them stays finite, as the maximum of the scores so far is never more than the score itself."""
+    p = Paged([(n, kv)], 8, 2, 128, 16, dtype)
+    t, q, k, v = p.seqs[0]
+    p.wide.fill_(1.0)
+    k, v = torch.zeros_like(k), torch.ones_like(v)
+    at = kv - n - 1
+    k[at], v[at] = 5 / 128 ** 0.5, 3e36
+    page = p.a.page_size
+    for j in range(kv):
+        p.kp[int(p.table[0, j // page]), :, j % page], p.vp[int(p.table[0, j // page]), :, j % page] = k[j], v[j]
+    p.seqs = [(t, q, k, v)]
+    p.call()
+    check_attention(p.out[:n], [(0, q, k, v)], p.dt)
+    assert B.llama_paged_status(p.st) == (B.LLAMA_OK, 0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_packed_values_that_are_not_finite(dtype):
     """The same over packed rows, K and V slices of one matrix, in the middle of a batch."""
     H, Hkv, D, lens = 8, 2, 128, [33, 290, 5]
